@@ -1,0 +1,414 @@
+"""Workloads of the 8-bit path: the root-mean-square norm with the residual's
+addition, the block-scaled 8-bit matrix product, and the same product grouped
+by expert, each with its gradient, in plain torch and through the library.
+
+8-bit tensors hold e4m3 values.  Activations carry one power of two for each
+128 columns of a row, weights one for each 128 x 128 block (e8m0), the
+smallest power of two that brings the group's largest magnitude to at most
+448.  Rows are padded with zeros to a multiple of 128 columns and rows of
+scales with ones to a multiple of 4 entries.
+
+Sizes: 2048, 11008 and 22016 are the hidden, MLP and gate|up widths of the
+benchmark's layer set, 8512 and 4096 those of its state-space layers, 25600
+tokens its longest prefill (50 x 512), 64 experts with 8 to a token the
+expert layout of the largest compressed model.
+"""
+
+import math
+
+import torch
+
+own = False
+
+E4M3 = torch.float8_e4m3fn
+E8M0 = torch.float8_e8m0fnu
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": E4M3}
+BYTES = {"f32": 4, "bf16": 2, "e4m3": 1}
+EPS = 1e-6
+
+
+def _up(n, m):
+    return -(-n // m) * m
+
+
+# ------------------------------------------------------------------ the cases
+
+def listed():
+    return [
+        # one token between two layers of a decode step: the smallest call, all latency
+        {"name": "norm-token", "op": "norm", "m": 1, "k": 2048, "x": "f32", "res": "bf16", "out": "e4m3"},
+        # the longest prefill: fp32 outputs of a layer into a bf16 residual stream and an 8-bit input
+        {"name": "norm-prefill", "op": "norm", "m": 25600, "k": 2048, "x": "f32", "res": "bf16", "out": "e4m3"},
+        # adapters trained through the layers: the norm's gradient, with the weight's
+        {"name": "norm-gradient", "op": "norm_bwd", "m": 2047, "k": 4096, "x": "f32", "res": "bf16"},
+        # decode: one token through gate|up, bound by the weight's bytes
+        {"name": "token-gate-up", "op": "linear", "m": 1, "n": 22016, "k": 2048, "x": "bf16", "y": "f32", "bias": False},
+        # a serving batch of odd size through down: few output columns, a long sum
+        {"name": "batch-down", "op": "linear", "m": 61, "n": 2048, "k": 11008, "x": "bf16", "y": "f32", "bias": True},
+        # prefill through gate|up: the product and its fp32 output cost about the same
+        {"name": "prefill-gate-up", "op": "linear", "m": 2048, "n": 22016, "k": 2048, "x": "bf16", "y": "f32", "bias": False},
+        # the longest prefill through down: bound by the matrix cores; the largest case
+        {"name": "long-down", "op": "linear", "m": 25600, "n": 2048, "k": 11008, "x": "bf16", "y": "bf16", "bias": True},
+        # the input gradient of a frozen state-space input projection (8512 outputs: ragged blocks)
+        {"name": "gradient-in-proj", "op": "linear_bwd", "m": 2047, "n": 8512, "k": 2048, "x": "f32", "y": "f32"},
+        # one token through the gate|up of its 8 experts
+        {"name": "token-experts", "op": "experts", "tokens": 1, "top": 8, "e": 64, "n": 2048, "k": 2048, "skew": 0.5, "x": "bf16", "y": "f32"},
+        # a serving batch: a few rows for each expert
+        {"name": "batch-experts", "op": "experts", "tokens": 61, "top": 8, "e": 64, "n": 2048, "k": 2048, "skew": 0.5, "x": "bf16", "y": "f32"},
+        # prefill: some 256 rows for each expert, ragged
+        {"name": "prefill-experts", "op": "experts", "tokens": 2048, "top": 8, "e": 64, "n": 2048, "k": 2048, "skew": 0.5, "x": "bf16", "y": "bf16"},
+        # adapters trained through frozen experts: the gradient of the second product's input
+        {"name": "gradient-experts", "op": "experts_bwd", "tokens": 512, "top": 8, "e": 64, "n": 2048, "k": 1024, "skew": 0.5, "x": "f32", "y": "f32"},
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "norm", "norm_bwd", "linear", "linear", "linear", "linear_bwd", "experts", "experts", "experts_bwd"])
+    if op in ("norm", "norm_bwd"):
+        k = _log(rng, 64, 11008)
+        if rng.random() < 0.5:
+            k = _up(k, 128)
+        m = _log(rng, 1, max(1, min(25600, 25600 * 2048 // k)))
+        case = {"op": op, "m": m, "k": k, "x": rng.choice(["f32", "bf16"]), "res": rng.choice(["f32", "bf16", "none"])}
+        if op == "norm":
+            case["out"] = rng.choice(["f32", "bf16", "e4m3", "e4m3"])
+        return case
+    if op in ("linear", "linear_bwd"):
+        n, k = _log(rng, 96, 22016), _log(rng, 96, 11008)
+        if rng.random() < 0.5:
+            n, k = _up(n, 64), _up(k, 64)
+        m = _log(rng, 1, max(1, min(25600, 25600 * 2048 * 11008 // (n * k))))
+        case = {"op": op, "m": m, "n": n, "k": k, "x": rng.choice(["bf16", "f32"]), "y": rng.choice(["f32", "bf16"])}
+        if op == "linear":
+            case["bias"] = rng.random() < 0.5
+        return case
+    e = rng.choice([8, 16, 32, 60, 64, 128])
+    n, k = _log(rng, 96, 2048), _log(rng, 96, 2048)
+    if rng.random() < 0.5:
+        n, k = _up(n, 64), _up(k, 64)
+    return {"op": op, "tokens": _log(rng, 1, 4096), "top": rng.choice([1, 2, 4, 8]), "e": e, "n": n, "k": k,
+            "skew": rng.choice([0.0, 0.5, 1.5]), "x": rng.choice(["bf16", "f32"]), "y": rng.choice(["f32", "bf16"])}
+
+
+# ----------------------------------------------------------------- the inputs
+
+def _exponent(a):
+    """The e8m0 byte of the smallest power of two p with a <= 448 p (1.75 * 2^8), from 2^-126 up."""
+    bits = a.contiguous().view(torch.int32)
+    return (((bits + 0x1FFFFF) >> 23) - 8).clamp(min=1)
+
+
+def _pow2(byte):
+    return (byte << 23).view(torch.float32)
+
+
+def _pad(x, rows, cols):
+    return torch.nn.functional.pad(x, (0, cols - x.shape[-1], 0, rows - x.shape[-2]))
+
+
+def _scales(byte):
+    """Exponent bytes as an e8m0 tensor whose rows are padded with ones (byte 127) to a multiple of 4."""
+    g = byte.shape[-1]
+    return torch.nn.functional.pad(byte, (0, _up(g, 4) - g), value=127).to(torch.uint8).view(E8M0)
+
+
+def _weight_8bit(w):
+    """w [..., n, k] as e4m3 [..., n, up(k, 128)] and e8m0 [..., blocks of n, up(blocks of k, 4)]."""
+    n, k = w.shape[-2:]
+    w = _pad(w, _up(n, 128), _up(k, 128))
+    b = w.unflatten(-1, (-1, 128)).unflatten(-3, (-1, 128))
+    byte = _exponent(b.abs().amax((-1, -3)))
+    q = b * _pow2(254 - byte)[..., :, None, :, None]
+    return q.flatten(-4, -3).flatten(-2)[..., :n, :].contiguous().to(E4M3), _scales(byte)
+
+
+def _transposed(q, s):
+    """The same values with rows and columns exchanged, padded anew; q is [..., n, k] without padding."""
+    n, k = q.shape[-2:]
+    qt = _pad(q.view(torch.uint8).transpose(-1, -2).contiguous(), k, _up(n, 128)).contiguous().view(E4M3)
+    byte = s.view(torch.uint8)[..., : -(-k // 128)].transpose(-1, -2).int()
+    return qt, _scales(byte)
+
+
+def _activations(gen, m, k, dtype):
+    """Hidden states: a few strong channels, and a row of zeros where a batch is padded."""
+    x = torch.randn(m, k, generator=gen, device="cuda")
+    x *= torch.exp(0.5 * torch.randn(k, generator=gen, device="cuda"))
+    x *= torch.where(torch.rand(k, generator=gen, device="cuda") < 0.002, 20.0, 1.0)
+    if m > 40:
+        x[m // 3] = 0
+    return x.to(dtype)
+
+
+def _weights(gen, *shape):
+    w = 0.02 * torch.randn(*shape, generator=gen, device="cuda")
+    return w * torch.where(torch.rand(*shape, generator=gen, device="cuda") < 0.001, 10.0, 1.0)
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(int(seed))
+    op, k = case["op"], case["k"]
+    s = {"op": op}
+    if op in ("norm", "norm_bwd"):
+        m, rdt = case["m"], case["res"]
+        s["weight"] = 1 + 0.2 * torch.randn(k, generator=gen, device="cuda")
+        if op == "norm":
+            s["x"] = _activations(gen, m, k, DTYPES[case["x"]])
+            s["residual"] = None if rdt == "none" else (2 * _activations(gen, m, k, torch.float32)).to(DTYPES[rdt])
+            s["out"] = DTYPES[case["out"]]
+        else:
+            # what the forward kept: its sum (or its input, where nothing was added) and 1 / rms
+            s["h"] = _activations(gen, m, k, DTYPES[case["x"] if rdt == "none" else rdt])
+            s["rstd"] = torch.rsqrt(s["h"].float().square().mean(-1) + EPS)
+            s["dy"] = (0.01 * torch.randn(m, k, generator=gen, device="cuda")).to(DTYPES[case["x"]])
+            s["dsum"] = None if rdt == "none" else 0.01 * torch.randn(m, k, generator=gen, device="cuda")
+        return s
+    n = case["n"]
+    s["y"] = DTYPES[case["y"]]
+    dtype = DTYPES[case["x"]]
+    if op in ("linear", "linear_bwd"):
+        q, sc = _weight_8bit(_weights(gen, n, k))
+        s["wq"], s["ws"] = q, sc
+        s["k"] = k
+        if op == "linear":
+            s["x"] = _activations(gen, case["m"], k, dtype)
+            s["bias"] = 0.01 * torch.randn(n, generator=gen, device="cuda") if case["bias"] else None
+        else:
+            s["dy"] = (0.01 * torch.randn(case["m"], n, generator=gen, device="cuda")).to(dtype)
+            s["wt"], s["wts"] = _transposed(q[:, :k], sc)
+        return s
+    # routing: every token's `top` distinct experts, some experts liked better
+    e, top, tokens = case["e"], min(case["top"], case["e"]), case["tokens"]
+    liked = torch.randn(tokens, e, generator=gen, device="cuda") + case["skew"] * torch.randn(e, generator=gen, device="cuda")
+    chosen = liked.topk(top, -1).indices.flatten()
+    order = chosen.sort(stable=True).indices
+    counts = torch.bincount(chosen, minlength=e)
+    s["rows"] = (order // top).int()
+    s["offsets"] = torch.nn.functional.pad(counts.cumsum(0), (1, 0)).int()
+    # the plan of the padded form: the experts that have rows, each row's place, the most rows of one
+    s["active"] = counts.nonzero().flatten()
+    s["place"] = (counts > 0).cumsum(0)[chosen[order]] - 1
+    s["slot"] = torch.arange(tokens * top, device="cuda") - s["offsets"][chosen[order]]
+    s["most"] = int(counts.max())
+    q, sc = _weight_8bit(_weights(gen, e, n, k))
+    s["wq"], s["ws"], s["k"] = q, sc, k
+    if op == "experts":
+        s["x"] = _activations(gen, tokens, k, dtype)
+    else:
+        s["dy"] = (0.01 * torch.randn(tokens * top, n, generator=gen, device="cuda")).to(dtype)
+        s["wt"], s["wts"] = _transposed(q[..., :k], sc)
+    return s
+
+
+# -------------------------------------------------------------- the plain form
+
+def _rows_8bit(x):
+    """x [m, k] in 32 bits as e4m3 values and exponent bytes, both padded."""
+    m, k = x.shape
+    g = _pad(x, m, _up(k, 128)).view(m, -1, 128)
+    byte = _exponent(g.abs().amax(-1))
+    return (g * _pow2(254 - byte)[..., None]).to(E4M3).view(m, -1), byte
+
+
+def _wide(q, byte):
+    """The values that rows of e4m3 with their exponent bytes stand for."""
+    return (q.float().view(q.shape[0], -1, 128) * _pow2(byte)[..., None]).view(q.shape)
+
+
+def _wide_weight(q, s):
+    n, kp = q.shape[-2:]
+    scale = s.float()[..., : kp // 128].repeat_interleave(128, -1).repeat_interleave(128, -2)
+    return q.float() * scale[..., :n, :]
+
+
+def _norm(s):
+    x = s["x"].float()
+    if s["residual"] is None:
+        kept = None
+    else:
+        kept = (x + s["residual"].float()).to(s["residual"].dtype)
+        x = kept.float()
+    rstd = torch.rsqrt(x.square().mean(-1) + EPS)
+    y = x * rstd[:, None] * s["weight"]
+    if s["out"] == E4M3:
+        q, byte = _rows_8bit(y)
+        return {"out": q, "scales": _scales(byte), "sum": kept, "rstd": rstd}
+    return {"out": y.to(s["out"]), "sum": kept, "rstd": rstd}
+
+
+def _norm_bwd(s):
+    h, dy, r = s["h"].float(), s["dy"].float(), s["rstd"][:, None]
+    g = dy * s["weight"]
+    dx = r * (g - h * (r * r * (g * h).mean(-1, keepdim=True)))
+    if s["dsum"] is not None:
+        dx = dx + s["dsum"]
+    return {"dx": dx, "dweight": (dy * h * r).sum(0)}
+
+
+def _linear(x, w, bias, dtype):
+    y = _wide(*_rows_8bit(x.float())) @ w.t()
+    return (y if bias is None else y + bias).to(dtype)
+
+
+def _experts(s, x, w, rows):
+    x = _wide(*_rows_8bit(x.float()))
+    padded = x.new_zeros(s["active"].numel(), s["most"], x.shape[1])
+    padded[s["place"], s["slot"]] = x if rows is None else x[rows.long()]
+    return torch.bmm(padded, w.transpose(1, 2).contiguous())[s["place"], s["slot"]].to(s["y"])
+
+
+def _own(s):
+    """The same through the library's entry points, as a user's program calls them."""
+    import vq_compressed_linear_amd as hx
+
+    def new(*shape, dtype=torch.float32):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+    op = s["op"]
+    if op == "norm":
+        x, res = s["x"], s["residual"]
+        m, k = x.shape
+        rstd = new(m)
+        kept = None if res is None else torch.empty_like(res)
+        if s["out"] == E4M3:
+            out, scales = new(m, _up(k, 128), dtype=E4M3), new(m, _up(-(-k // 128), 4), dtype=E8M0)
+        else:
+            out, scales = new(m, k, dtype=s["out"]), None
+        hx.hxq_rms_norm(x, s["weight"], EPS, out, scales=scales, residual=res, residual_out=kept, rstd=rstd)
+        return {"out": out, "sum": kept, "rstd": rstd} if scales is None else {"out": out, "scales": scales, "sum": kept, "rstd": rstd}
+    if op == "norm_bwd":
+        m, k = s["h"].shape
+        dx, dweight = new(m, k), new(k)
+        hx.hxq_rms_norm_bwd(s["dy"], s["h"], s["weight"], s["rstd"], dx, dweight=dweight, dresidual=s["dsum"])
+        return {"dx": dx, "dweight": dweight}
+    if op == "linear":
+        y = new(s["x"].shape[0], s["wq"].shape[0], dtype=s["y"])
+        hx.hxq_linear_fwd_fp8(s["x"], None, s["wq"], s["ws"], s["bias"], y)
+    elif op == "linear_bwd":
+        y = new(s["dy"].shape[0], s["k"], dtype=s["y"])
+        hx.hxq_linear_fwd_fp8(s["dy"], None, s["wt"], s["wts"], None, y)
+    elif op == "experts":
+        y = new(s["rows"].shape[0], s["wq"].shape[1], dtype=s["y"])
+        hx.hxq_linear_fwd_fp8_experts(s["x"], None, s["rows"], s["offsets"], s["wq"], s["ws"], None, y)
+    else:
+        y = new(s["dy"].shape[0], s["k"], dtype=s["y"])
+        hx.hxq_linear_fwd_fp8_experts(s["dy"], None, None, s["offsets"], s["wt"], s["wts"], None, y)
+    return y
+
+
+def run(state):
+    if own:
+        return _own(state)
+    op = state["op"]
+    if op == "norm":
+        return _norm(state)
+    if op == "norm_bwd":
+        return _norm_bwd(state)
+    if op == "linear":
+        return _linear(state["x"], _wide_weight(state["wq"], state["ws"]), state["bias"], state["y"])
+    if op == "linear_bwd":
+        w = _wide_weight(state["wq"], state["ws"])[:, : state["k"]].t()
+        return _linear(state["dy"], _pad(w, w.shape[0], _up(w.shape[1], 128)), None, state["y"])
+    # only the experts that have rows
+    q, scales = state["wq"].view(torch.uint8)[state["active"]], state["ws"].view(torch.uint8)[state["active"]]
+    w = _wide_weight(q.view(E4M3), scales.view(E8M0))
+    if op == "experts":
+        return _experts(state, state["x"], w, state["rows"])
+    w = w[..., : state["k"]].transpose(1, 2)
+    return _experts(state, state["dy"], _pad(w, w.shape[1], _up(w.shape[2], 128)), None)
+
+
+# ------------------------------------------------------------------- the floor
+
+def work(case):
+    op, k = case["op"], case["k"]
+    if op in ("norm", "norm_bwd"):
+        m = case["m"]
+        x = BYTES[case["x"]]
+        res = 0 if case["res"] == "none" else BYTES[case["res"]]
+        if op == "norm":
+            return {"bytes": m * k * (x + 2 * res + BYTES[case["out"]]) + 4 * k + 4 * m, "flops": 6 * m * k}
+        return {"bytes": m * k * (x + (res or x) + (4 if res else 0) + 4) + 8 * k + 4 * m, "flops": 10 * m * k}
+    n = case["n"]
+    a, b = (k, n) if op in ("linear", "experts") else (n, k)  # the sum's length, the output's width
+    x, y = BYTES[case["x"]], BYTES[case["y"]]
+    if op in ("linear", "linear_bwd"):
+        m = case["m"]
+        return {"bytes": n * k + m * (a * x + b * y), "flops": 2 * m * n * k}
+    top = min(case["top"], case["e"])
+    rows, tokens = case["tokens"] * top, case["tokens"]
+    active = case["e"] * (1 - (1 - top / case["e"]) ** tokens)  # experts that some token chose, where none is liked better
+    read = tokens if op == "experts" else rows
+    return {"bytes": active * n * k + read * a * x + rows * b * y, "flops": 2 * rows * n * k}
+
+
+# -------------------------------------------------------------- the definition
+
+def _exact_power(a):
+    """The smallest power of two p >= 2^-126 with a <= 448 p, by its logarithm."""
+    e = torch.ceil(torch.log2(torch.clamp(a, min=1e-300) / 448))
+    e = torch.where(a > 448 * torch.exp2(e), e + 1, e)
+    e = torch.where(a <= 448 * torch.exp2(e - 1), e - 1, e)
+    return torch.exp2(torch.clamp(e, min=-126))
+
+
+def _exact_rows(x, rounded=True):
+    """(values over their powers of two, the powers), in 64 bits; `rounded`: to e4m3's 3 bits after the
+    leading one and its smallest step of 2^-9, ties to even."""
+    m, k = x.shape
+    x = torch.cat([x, x.new_zeros(m, -k % 128)], 1).reshape(m, -1, 128)
+    p = _exact_power(x.abs().amax(2))
+    v = x / p[:, :, None]
+    if rounded:
+        step = torch.exp2(torch.clamp(torch.floor(torch.log2(torch.clamp(v.abs(), min=2.0**-9))), min=-6) - 3)
+        v = torch.round(v / step) * step
+    return v, p
+
+
+def _exact_wide(q, s):
+    n, kp = q.shape
+    block_r, block_c = torch.arange(n, device=q.device) // 128, torch.arange(kp, device=q.device) // 128
+    return q.double() * s.double()[block_r][:, block_c]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = s["op"]
+    if op == "norm":
+        x = s["x"].double()
+        out = {"sum": None}
+        if s["residual"] is not None:
+            out["sum"] = x + s["residual"].double()
+            # the norm is of the sum as it is kept, in the residual's type
+            x = (s["x"].float() + s["residual"].float()).to(s["residual"].dtype).double()
+        out["rstd"] = 1 / torch.sqrt((x * x).sum(1) / x.shape[1] + EPS)
+        y = x * out["rstd"][:, None] * s["weight"].double()
+        if s["out"] != E4M3:
+            return {**out, "out": y}
+        v, p = _exact_rows(y, rounded=False)
+        ones = p.new_ones(p.shape[0], -p.shape[1] % 4)
+        return {**out, "out": v.reshape(v.shape[0], -1), "scales": torch.cat([p, ones], 1)}
+    if op == "norm_bwd":
+        h, dy, w, r = s["h"].double(), s["dy"].double(), s["weight"].double(), s["rstd"].double()
+        dot = (dy * w * h).sum(1) / h.shape[1]
+        dx = (dy * w) * r[:, None] - h * (dot * r**3)[:, None]
+        return {"dx": dx if s["dsum"] is None else dx + s["dsum"].double(), "dweight": torch.mv((dy * h).t(), r)}
+    x = s["x"] if "x" in s else s["dy"]
+    v, p = _exact_rows(x.double())
+    x = (v * p[:, :, None]).reshape(x.shape[0], -1)
+    if op == "linear":
+        y = x @ _exact_wide(s["wq"], s["ws"]).t()
+        return y if s["bias"] is None else y + s["bias"].double()
+    if op == "linear_bwd":
+        return x[:, : s["wq"].shape[0]] @ _exact_wide(s["wq"], s["ws"])[:, : s["k"]]
+    ends = s["offsets"].tolist()
+    parts = []
+    for e in range(len(ends) - 1):
+        at = slice(ends[e], ends[e + 1])
+        w = _exact_wide(s["wq"][e], s["ws"][e])
+        parts.append(x[s["rows"][at].long()] @ w.t() if op == "experts" else x[at, : w.shape[0]] @ w[:, : s["k"]])
+    return torch.cat(parts)
