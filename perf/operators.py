@@ -45,8 +45,8 @@ def listed():
         {"name": "token-gate-up", "op": "linear", "m": 1, "n": 22016, "k": 2048, "x": "bf16", "y": "f32", "bias": False},
         # a serving batch of odd size through down: few output columns, a long sum
         {"name": "batch-down", "op": "linear", "m": 61, "n": 2048, "k": 11008, "x": "bf16", "y": "f32", "bias": True},
-        # prefill through gate|up: the product and its fp32 output cost about the same
-        {"name": "prefill-gate-up", "op": "linear", "m": 2048, "n": 22016, "k": 2048, "x": "bf16", "y": "f32", "bias": False},
+        # prefill through gate|up, between bf16 activations: a short sum, so the output's bytes count too
+        {"name": "prefill-gate-up", "op": "linear", "m": 2048, "n": 22016, "k": 2048, "x": "bf16", "y": "bf16", "bias": False},
         # the longest prefill through down: bound by the matrix cores; the largest case
         {"name": "long-down", "op": "linear", "m": 25600, "n": 2048, "k": 11008, "x": "bf16", "y": "bf16", "bias": True},
         # the input gradient of a frozen state-space input projection (8512 outputs: ragged blocks)
