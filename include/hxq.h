@@ -79,7 +79,8 @@ enum hxq_status {
   HXQ_ERR_SCRATCH = -7      /* hxq_linear_bwd_x_noalloc: the call needs more than HXQ_SCRATCH_BYTES */
 };
 
-enum hxq_dtype { HXQ_F32 = 0, HXQ_BF16 = 1 };
+/* HXQ_E4M3 is taken by the 8-bit path's entry points only. */
+enum hxq_dtype { HXQ_F32 = 0, HXQ_BF16 = 1, HXQ_E4M3 = 2 };
 
 /* Forward pass, 1D VQ (u8).
  *   codebook  [256] float32 (model cards, "What is HelixCode?").
@@ -417,6 +418,158 @@ int hxq_linear_fwd_pk12_ex(const float* codebook2, const uint8_t* packed,
 /* The kernel family AUTO picks for these arguments (an hxq_variant), or a
  * negative hxq_status if the call would be rejected.  Host only. */
 int hxq_select_variant(int fmt_pk12, int x_dtype, int64_t M, int64_t N, int64_t K);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit path: rows and layers held in e4m3 with power-of-two block scales.
+ *
+ * A third layer format beside u8 and pk12, one byte per weight, whose operand
+ * needs no gather: products run on the 8-bit matrix cores.  A layer is laid
+ * out once, from a dense weight (hxq_quant_fp8_weight), which may be a u8 or
+ * pk12 layer's (hxq_dequant_bf16).
+ *
+ * Layouts (all contiguous)
+ *   - values: e4m3 bytes (OCP: largest 448, 0x7f / 0xff NaN, no infinities),
+ *     rows padded with zeros to Kp = 128 * ceil(K / 128) columns.
+ *   - scales: e8m0 bytes b, standing for 2^(b - 127).  Activations [M][Kp]
+ *     have one for each 128 columns of a row, [M][Gs]; weights [N][Kp] one for
+ *     each 128 x 128 block, [ceil(N / 128)][Gs].  Gs = 4 * ceil(K / 512): rows
+ *     of scales are padded to a multiple of 4 with 127 (one).
+ *   - a group's scale is the smallest power of two p >= 2^-126 with
+ *     a <= 448 p, a the largest finite magnitude of the group; its values are
+ *     v / p rounded to e4m3 (nearest, ties to even).  Infinities and NaN
+ *     become NaN and take no part in the scale.
+ *   - experts: E weights of the same N x K one after another, [E][N][Kp] and
+ *     [E][ceil(N / 128)][Gs].
+ * Alignment: e4m3 values 16 bytes, scales 4, fp32 and int32 arrays 4, float32
+ * and bf16 matrices their element size; workspaces 16.
+ * ------------------------------------------------------------------------ */
+
+/* x [M][K] float32 or bf16 as e4m3 rows: q [M][Kp], scales [M][Gs], both
+ * overwritten, padding included.  M == 0 or K == 0 does nothing.
+ * Errors: HXQ_ERR_DTYPE, HXQ_ERR_SHAPE, HXQ_ERR_NULL, HXQ_ERR_ALIGN. */
+int hxq_quant_fp8(const void* x, int x_dtype, uint8_t* q, uint8_t* scales, int64_t M, int64_t K, hipStream_t stream);
+
+/* Weights w [E][N][K] float32 or bf16 as e4m3 with 128 x 128 scales: q
+ * [E][N][Kp], scales [E][ceil(N / 128)][Gs]; with qt and scales_t (both or
+ * neither) also the transposed copy, the same values and scales with N and K
+ * exchanged: qt [E][K][Np], scales_t [E][ceil(K / 128)][Gs of N].  A product
+ * with the transposed copy is a product with W itself: the input gradient of
+ * the layer.  N == 0 or K == 0 does nothing.
+ * Errors: HXQ_ERR_DTYPE; HXQ_ERR_SHAPE (E outside 1 .. 65535, or more than
+ * 2^23 blocks); HXQ_ERR_NULL; HXQ_ERR_ALIGN. */
+int hxq_quant_fp8_weight(const void* w, int w_dtype, uint8_t* q, uint8_t* scales, uint8_t* qt, uint8_t* scales_t,
+                         int64_t E, int64_t N, int64_t K, hipStream_t stream);
+
+/* Forward pass of an 8-bit layer:
+ *
+ *     y[m][n] = bias[n] + sum_k (qx[m][k] px[m][k / 128]) (qw[n][k] pw[n / 128][k / 128])
+ *
+ * (HXQ whitepaper, "Method": a linear layer computed from its compressed
+ * weight; the 8-bit form is this library's addition.)  It is also the input
+ * gradient of a frozen layer (model cards, "Good to Know": adapters train
+ * through it): with dy as x and the transposed copy as the weight.
+ *   x         HXQ_E4M3: values [M][Kp] with x_scales [M][Gs]; HXQ_F32 or
+ *             HXQ_BF16: [M][K], converted as hxq_quant_fp8 does (x_scales is
+ *             not read).
+ *   wq, w_scales  the layer; bias [N] float32 or NULL.
+ *   y         [M][N] float32 or bf16 (y_dtype), overwritten; must not overlap
+ *             any input.
+ *   workspace caller-owned device memory of at least the size
+ *             hxq_linear_fwd_fp8_workspace gives (the converted x; partial
+ *             sums where the sum over k is split over workgroups); contents on
+ *             entry ignored and on return unspecified.  Two calls that may run
+ *             at once need one each, captured graphs among them.
+ * Arithmetic: with float32 y the 8-bit values are multiplied exactly and
+ * summed in fp32 (widened to bf16, on the bf16 matrix cores).  With bf16 y
+ * past 64 rows the 8-bit matrix cores may multiply, at twice the rate: they
+ * keep a product only down to 2^-13 of the largest of its group of 8 (1.5e-5
+ * of the result, measured; bf16's own rounding is 2^-9 of it).  Partial sums
+ * are added in a fixed order; bf16 y is rounded once.  A NaN in x makes its
+ * whole row of y NaN and no other.  K == 0: y = bias (or 0).
+ * Errors: HXQ_ERR_DTYPE; HXQ_ERR_SHAPE (also more than 2^22 tiles of y);
+ * HXQ_ERR_NULL; HXQ_ERR_ALIGN; HXQ_ERR_UNSUPPORTED for a workspace smaller
+ * than the query gives. */
+int hxq_linear_fwd_fp8(const void* x, int x_dtype, const uint8_t* x_scales, const uint8_t* wq,
+                       const uint8_t* w_scales, const float* bias, void* y, int y_dtype, int64_t M, int64_t N,
+                       int64_t K, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace hxq_linear_fwd_fp8 needs on the current device, or a
+ * negative hxq_status for arguments it would reject.  Host only. */
+int64_t hxq_linear_fwd_fp8_workspace(int x_dtype, int64_t M, int64_t N, int64_t K);
+
+/* The same product for rows grouped by expert (a mixture layer whose experts
+ * are compressed one by one), all experts in one launch: row r of y with
+ * offsets[e] <= r < offsets[e + 1] is
+ *
+ *     y[r] = bias[e] + W_e x[rows[r]]            (x[r] with rows NULL)
+ *
+ *   offsets   [E + 1] int32 on the device, non-decreasing, offsets[0] = 0,
+ *             offsets[E] <= M; an expert may have no rows.  Rows of y from
+ *             offsets[E] on are left as they are.
+ *   rows      [M] int32 on the device or NULL (then M_x == M): the row of
+ *             x [M_x] that each row of y reads, any order, repeats allowed, so
+ *             a token's row is converted and stored once for all its experts.
+ *             Entries past offsets[E] are not read.  Entries outside
+ *             0 .. M_x - 1 and offsets that break their rule give unspecified
+ *             values in y, and never an access outside the tensors.
+ *   bias      [E][N] or NULL; the rest as for hxq_linear_fwd_fp8.
+ * The input gradient is the same call with dy as x, rows NULL and the
+ * transposed copies.
+ * Errors: those of hxq_linear_fwd_fp8; HXQ_ERR_SHAPE for E outside 1 .. 65535
+ * or M_x != M without rows. */
+int hxq_linear_fwd_fp8_experts(const void* x, int x_dtype, const uint8_t* x_scales, const int32_t* rows,
+                               const int32_t* offsets, const uint8_t* wq, const uint8_t* w_scales, const float* bias,
+                               void* y, int y_dtype, int64_t M_x, int64_t M, int64_t E, int64_t N, int64_t K,
+                               void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+int64_t hxq_linear_fwd_fp8_experts_workspace(int x_dtype, int64_t M_x, int64_t M, int64_t E, int64_t N, int64_t K);
+
+/* Root-mean-square norm with the residual's addition, the step between one
+ * layer's float32 output and the next layer's input:
+ *
+ *     h = x + residual;  r = 1 / sqrt(mean_k h^2 + eps);  out = h r weight
+ *
+ *   x            [M][K] float32 or bf16.
+ *   residual     [M][K] float32 or bf16 (residual_dtype) or NULL (h = x).
+ *   residual_out [M][K] of residual_dtype, required with a residual and only
+ *                then: h, rounded to that type.  The norm is of the rounded h,
+ *                so the gradient sees the same values.  May be residual itself.
+ *   weight       [K] float32 or NULL (ones).
+ *   out          out_dtype HXQ_F32 or HXQ_BF16: [M][K] (the u8 and pk12 layers'
+ *                input); HXQ_E4M3: [M][Kp] with scales [M][Gs] (the 8-bit
+ *                layers' input), converted from the float32 result as
+ *                hxq_quant_fp8 does.  scales is not used otherwise.
+ *   rstd         [M] float32, receives r; or NULL.
+ * Statistics are fp32.  M == 0 or K == 0 does nothing.
+ * Errors: HXQ_ERR_DTYPE; HXQ_ERR_SHAPE; HXQ_ERR_NULL; HXQ_ERR_ALIGN;
+ * HXQ_ERR_UNSUPPORTED for a negative or NaN eps. */
+int hxq_rms_norm(const void* x, int x_dtype, const void* residual, int residual_dtype, const float* weight, float eps,
+                 void* residual_out, void* out, int out_dtype, uint8_t* scales, float* rstd, int64_t M, int64_t K,
+                 hipStream_t stream);
+
+/* Gradient of hxq_rms_norm (of its float32 result: an 8-bit output passes its
+ * gradient through unchanged), with g = dy weight:
+ *
+ *     dx = r (g - h r^2 mean_k(g h)) + dresidual;   dweight = sum_m dy h r
+ *
+ *   dy         [M][K] float32 or bf16.
+ *   h          [M][K] float32 or bf16: the forward's residual_out, or its x
+ *              without a residual.  rstd [M]: as the forward gave it.
+ *   dresidual  [M][K] float32 or NULL: the gradient that reaches residual_out
+ *              from its other readers.
+ *   dx         [M][K] float32, overwritten: the gradient of x, and of residual
+ *              (they are the same).  May be dresidual itself.
+ *   dweight    [K] float32, overwritten, or NULL.
+ *   workspace  hxq_rms_norm_bwd_workspace bytes when dweight is given (partial
+ *              sums, added in a fixed order); as for hxq_linear_fwd_fp8.
+ * M == 0: dweight is set to zero.  K == 0 does nothing.
+ * Errors: HXQ_ERR_DTYPE, HXQ_ERR_SHAPE, HXQ_ERR_NULL, HXQ_ERR_ALIGN,
+ * HXQ_ERR_UNSUPPORTED for a workspace that is too small. */
+int hxq_rms_norm_bwd(const void* dy, int dy_dtype, const void* h, int h_dtype, const float* weight, const float* rstd,
+                     const float* dresidual, float* dx, float* dweight, int64_t M, int64_t K, void* workspace,
+                     int64_t workspace_bytes, hipStream_t stream);
+
+int64_t hxq_rms_norm_bwd_workspace(int64_t M, int64_t K);
 
 /* Static text for a status code. */
 const char* hxq_status_str(int status);

@@ -1,0 +1,596 @@
+"""The 8-bit path on the GPU against the oracle in 64 bits.
+
+Tolerances.  Conversion to e4m3 is exact arithmetic (a power of two) and one
+rounding, so bytes and scales have to be equal.  Products of e4m3 values are
+exact in fp32, their sum is fp32: 1e-5 of |x| |w|^T, the library's bound for
+fp32 sums (sqrt(K) 2^-24 at the largest K here is 6e-6); bf16 results add half
+a step, 2^-8 of the value, and past 64 rows 2^-10 of |x| |w|^T: there the 8-bit
+matrix cores may lose each of a group's 8 products below 2^-13 of the largest.  The norm's statistics are sums of positive terms
+in chains of at most K / 64 + 16 additions: each adds 2^-24 relative, half of
+it after the square root, and six more roundings follow.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import vq_compressed_linear_amd as hx
+from hxq_synth import gen
+from oracle import fp8_oracle as O
+
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+E4, E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+F32, BF16 = torch.float32, torch.bfloat16
+U = 2.0**-24
+HALF = {F32: 0.0, BF16: 2.0**-8}
+
+
+def up(n, m):
+    return -(-n // m) * m
+
+
+def host(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def raw(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def make(seed, *shape, dtype=F32, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(*shape, generator=g) * torch.exp(0.7 * torch.randn(shape[-1], generator=g)) * scale
+    return x.to(dtype).cuda()
+
+
+def rows8(x):
+    q = torch.full((x.shape[0], up(x.shape[1], 128)), float("nan"), device="cuda").to(E4)
+    s = torch.full((x.shape[0], up(-(-x.shape[1] // 128), 4)), 255, dtype=torch.uint8, device="cuda").view(E8)
+    hx.hxq_quant_fp8(x, q, s)
+    return q, s
+
+
+def weight8(w, transposed=False):
+    lead, (n, k) = w.shape[:-2], w.shape[-2:]
+
+    def new(n, k):
+        return (torch.full(lead + (n, up(k, 128)), 0x55, dtype=torch.uint8, device="cuda").view(E4),
+                torch.full(lead + (-(-n // 128), up(-(-k // 128), 4)), 255, dtype=torch.uint8, device="cuda").view(E8))
+
+    a = new(n, k)
+    b = new(k, n) if transposed else (None, None)
+    hx.hxq_quant_fp8_weight(w, *a, *b)
+    return (*a, *b) if transposed else a
+
+
+def near(got, want, bound, what=""):
+    got = host(got)
+    assert got.shape == want.shape
+    bad = ~(np.abs(got - want) <= bound)
+    assert not bad.any(), "%s: %d of %d off, worst %.3g of its bound, first at %s: %r for %r" % (
+        what, bad.sum(), bad.size, np.max(np.abs(got - want) / np.maximum(bound, 1e-300)), np.argwhere(bad)[0],
+        got[bad][0], want[bad][0])
+
+
+# ------------------------------------------------------------------ conversion
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,K", [(1, 1), (3, 7), (2, 128), (5, 129), (7, 513), (64, 2048), (33, 2050), (2, 20000)])
+def test_rows(M, K, dtype):
+    x = make(M * 1000 + K, M, K, dtype=dtype)
+    if M > 2:
+        x[1] = 0
+        x[2, ::3] *= 1e-30
+    q, s = rows8(x)
+    Q, S = O.quant_rows(host(x))
+    assert np.array_equal(raw(q), Q) and np.array_equal(raw(s), S)
+
+
+def test_rows_of_special_values():
+    x = torch.zeros(9, 256)
+    x[0, 0], x[0, 5], x[0, 130] = float("inf"), 3.0, -float("inf")
+    x[1, 0], x[1, 1] = float("nan"), -1e-3
+    x[2] = torch.finfo(F32).max
+    x[3] = torch.finfo(F32).tiny / 4  # subnormal
+    x[4, :8] = torch.tensor([448.0, 449, 448 * 2.0**-126, 1e-45, -448, 17, 18, 19])
+    x[5] = -0.0
+    x[6, 7] = 1.75 * 2.0**-118  # 448 2^-126: the smallest scale's largest value
+    x[7, 7] = 1.7500001
+    x[8] = 1e-45
+    q, s = rows8(x.cuda())
+    Q, S = O.quant_rows(x.numpy())
+    assert np.array_equal(raw(s), S)
+    assert np.array_equal(O.E4M3[raw(q)], O.E4M3[Q], equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(1, 1), (128, 128), (127, 129), (300, 70), (5, 1000), (2, 130, 250), (3, 128, 64)])
+def test_weight_and_its_transpose(shape, dtype):
+    w = make(sum(shape), *shape, dtype=dtype, scale=0.02)
+    q, s, qt, st = weight8(w, transposed=True)
+    q1, s1 = weight8(w)
+    assert torch.equal(q.view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s.view(torch.uint8), s1.view(torch.uint8))
+    lead = (1,) if w.dim() == 2 else (w.shape[0],)
+    flat = [t.reshape(lead + t.shape[-2:]) for t in (w, q, s, qt, st)]
+    for e in range(lead[0]):
+        W, *got = [t[e] for t in flat]
+        Q, S = O.quant_weight(host(W))
+        assert np.array_equal(raw(got[0]), Q) and np.array_equal(raw(got[1]), S)
+        n, k = W.shape
+        T = np.zeros((k, up(n, 128)), dtype=np.uint8)
+        T[:, :n] = Q[:, :k].T
+        G = np.full((-(-k // 128), up(-(-n // 128), 4)), 127, dtype=np.uint8)
+        G[:, : S.shape[0]] = S[:, : -(-k // 128)].T
+        assert np.array_equal(raw(got[2]), T) and np.array_equal(raw(got[3]), G)
+
+
+# -------------------------------------------------------------------- products
+
+def product_bound(Y, B, y_dtype):
+    return (1e-5 if y_dtype == F32 else 2.0**-10) * B + (U + HALF[y_dtype]) * np.abs(Y)
+
+
+def check_linear(M, N, K, x_dtype=BF16, y_dtype=F32, bias=True, seed=0, pair=False):
+    say("linear", M, N, K, x_dtype, y_dtype, bias, pair)
+    x = make(seed + 1, M, K, dtype=x_dtype)
+    q, s = weight8(make(seed + 2, N, K, scale=0.02))
+    b = make(seed + 3, N) if bias else None
+    y = torch.full((M, N), float("nan"), dtype=y_dtype, device="cuda")
+    xq, xs = rows8(x)
+    hx.hxq_linear_fwd_fp8(xq if pair else x, xs if pair else None, q, s, b, y)
+    Y, B = O.linear(O.wide_rows(raw(xq), raw(xs)), O.wide_weight(raw(q), raw(s)), None if b is None else host(b))
+    near(y, Y, product_bound(Y, B, y_dtype), "linear")
+    return x, q, s, b, y
+
+
+@pytest.mark.parametrize("K", [1, 127, 128, 130, 1024, 2048, 4300])
+@pytest.mark.parametrize("M,N", [(1, 1), (1, 300), (2, 17), (16, 256), (17, 200), (32, 64), (33, 129), (61, 2048), (64, 96)])
+def test_linear_few_rows(M, N, K):
+    check_linear(M, N, K, x_dtype=BF16 if K % 2 else F32, bias=bool(N % 2))
+
+
+@pytest.mark.parametrize("M,N,K", [(65, 130, 256), (128, 128, 128), (200, 257, 384), (255, 512, 130), (256, 256, 2048),
+                                   (257, 1000, 640), (500, 300, 1100), (1024, 512, 512), (300, 2048, 4224), (700, 260, 1)])
+@pytest.mark.parametrize("y_dtype", [F32, BF16])
+def test_linear_many_rows(M, N, K, y_dtype):
+    check_linear(M, N, K, y_dtype=y_dtype, bias=bool(M % 2), pair=y_dtype == BF16)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 22016, 2048), (8, 2048, 11008), (61, 2048, 11008), (512, 2048, 2048)])
+def test_linear_layer_shapes(M, N, K):
+    check_linear(M, N, K, seed=5)
+
+
+def test_linear_without_a_sum():
+    w, s = torch.zeros((5, 0), dtype=torch.uint8, device="cuda").view(E4), torch.zeros((1, 0), dtype=torch.uint8, device="cuda").view(E8)
+    b, y = make(1, 5), torch.full((3, 5), float("nan"), device="cuda")
+    hx.hxq_linear_fwd_fp8(torch.zeros((3, 0), device="cuda"), None, w, s, b, y)
+    assert torch.equal(y, b.expand(3, 5))
+    hx.hxq_linear_fwd_fp8(torch.zeros((3, 0), device="cuda"), None, w, s, None, y)
+    assert not y.any()
+    hx.hxq_linear_fwd_fp8(torch.zeros((0, 0), device="cuda"), None, w, s, None, y[:0])
+
+
+@pytest.mark.parametrize("M", [1, 20, 60, 300])
+def test_linear_with_nan_rows_keeps_them_apart(M):
+    """A NaN (or infinity) in x makes its own row of y NaN and no other."""
+    x, q, s, b, y = check_linear(M, 200, 300)
+    x2 = x.clone()
+    x2[M // 2, 7] = float("inf") if M % 2 else float("nan")
+    y2 = torch.empty_like(y)
+    hx.hxq_linear_fwd_fp8(x2, None, q, s, b, y2)
+    keep = torch.arange(M, device="cuda") != M // 2
+    assert torch.equal(y2[keep], y[keep]) and y2[M // 2].isnan().all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 600, 4300), (48, 130, 5000), (300, 260, 640)])
+def test_linear_is_deterministic_and_takes_a_workspace(M, N, K):
+    x, q, s, b, y = check_linear(M, N, K)
+    need = hx.lib().hxq_linear_fwd_fp8_workspace(hx.HXQ_BF16, M, N, K)
+    w = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        y2 = torch.empty_like(y)
+        hx.hxq_linear_fwd_fp8(x, None, q, s, b, y2, workspace=w)
+        assert torch.equal(y, y2)
+        w[:need].random_()
+        assert (w[need:] == 255).all()  # nothing past what it asked for
+    with pytest.raises(hx.HxqError):
+        hx.hxq_linear_fwd_fp8(x, None, q, s, b, y2, workspace=w[: need - 1])
+    with pytest.raises(hx.HxqError):
+        hx.hxq_linear_fwd_fp8(x, None, q, s, b, y2, workspace=w[:0])
+
+
+def test_linear_extreme_scales():
+    """Weights and rows whose powers of two are far apart."""
+    M, N, K = 20, 140, 384
+    x = make(1, M, K)
+    x[:, :128] *= 1e-12
+    x[:, 128:256] *= 1e12
+    w = make(2, N, K)
+    w[:, :128] *= 1e12
+    w[:, 128:256] *= 1e-12
+    q, s = weight8(w)
+    y = torch.empty((M, N), device="cuda")
+    xq, xs = rows8(x)
+    hx.hxq_linear_fwd_fp8(x, None, q, s, None, y)
+    Y, B = O.linear(O.wide_rows(raw(xq), raw(xs)), O.wide_weight(raw(q), raw(s)))
+    near(y, Y, 1e-5 * B)
+
+
+# --------------------------------------------------------------------- experts
+
+def routing(seed, counts, Mx, tail=0):
+    rng = np.random.default_rng(seed)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    rows = rng.integers(0, Mx, offsets[-1] + tail)
+    return torch.from_numpy(rows).int().cuda(), torch.from_numpy(offsets).int().cuda()
+
+
+CASES = [
+    # counts, rows of x, N, K
+    ([1], 1, 40, 128),
+    ([0, 0, 3, 0], 5, 100, 200),
+    ([1, 1, 1, 1, 1, 1, 1, 1] + [0] * 56, 1, 256, 512),
+    ([5, 0, 17, 40, 1, 0, 64, 33], 30, 200, 300),
+    ([100, 0, 3, 257, 300, 0], 128, 130, 640),
+    ([0] * 130 + [9] + [0] * 5 + [3], 4, 64, 256),
+    ([2000, 1, 0, 90], 700, 300, 384),
+    ([300] * 10, 500, 256, 256),
+    ([0, 0, 0], 3, 64, 128),
+]
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_experts(i, gather):
+    counts, Mx, N, K = CASES[i]
+    tail = i % 3 * 5  # rows past the last expert's
+    E, M = len(counts), sum(counts) + tail
+    say("experts", counts[:10], Mx, N, K, gather, tail)
+    y_dtype = BF16 if i % 2 else F32
+    rows, offsets = routing(i, counts, Mx, tail)
+    rows[M - tail:] = 2**30  # never read
+    x = make(i, Mx if gather else M, K, dtype=F32 if i % 2 else BF16)
+    q, s = weight8(make(i + 50, E, N, K, scale=0.02))
+    b = make(i + 60, E, N) if i % 2 else None
+    y = torch.full((M, N), 7.0, dtype=y_dtype, device="cuda")
+    hx.hxq_linear_fwd_fp8_experts(x, None, rows if gather else None, offsets, q, s, b, y)
+    xq, xs = rows8(x) if M else (None, None)
+    n = sum(counts)
+    assert (y[n:] == 7.0).all()
+    if n:
+        Y, B = O.experts(O.wide_rows(raw(xq), raw(xs)), rows.cpu().numpy() if gather else None, offsets.tolist(),
+                         [O.wide_weight(raw(q[e]), raw(s[e])) for e in range(E)], None if b is None else host(b))
+        near(y[:n], Y, product_bound(Y, B, y_dtype), "experts")
+
+
+def test_experts_deterministic_with_a_split_sum():
+    """Few tiles and a long sum: the parts go through the workspace, rows past the end stay."""
+    counts, K, N = [3, 0, 2], 9000, 48
+    rows, offsets = routing(3, counts, 4, 2)
+    rows[5:] = -5
+    x, (q, s), b = make(1, 4, K), weight8(make(2, 3, N, K)), make(3, 3, N)
+    out = []
+    for _ in range(3):
+        y = torch.full((7, N), 7.0, device="cuda")
+        hx.hxq_linear_fwd_fp8_experts(x, None, rows, offsets, q, s, b, y)
+        out.append(y)
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2]) and (out[0][5:] == 7.0).all()
+    xq, xs = rows8(x)
+    Y, B = O.experts(O.wide_rows(raw(xq), raw(xs)), rows.cpu().numpy(), offsets.tolist(),
+                     [O.wide_weight(raw(q[e]), raw(s[e])) for e in range(3)], host(b))
+    near(out[0][:5], Y, 1e-5 * B + U * np.abs(Y))
+
+
+def test_experts_bad_indices_stay_inside():
+    """Rows out of range and offsets that break their rule: unspecified values, no access outside."""
+    x, (q, s) = make(1, 6, 256), weight8(make(2, 4, 64, 256))
+    guard = torch.full((20 + 9 + 20, 64), 7.0, device="cuda")
+    y = guard[20:29]
+    rows = torch.tensor([0, -1, 2**31 - 1, -(2**31), 6, 5, 3, 2, 1], dtype=torch.int32, device="cuda")
+    for off in ([0, 3, 5, 7, 9], [0, 100, 2**31 - 1, 5, 9], [-5, 4, -(2**31), 9, 9], [9, 7, 5, 3, 0], [3, 3, 3, 3, 3]):
+        hx.hxq_linear_fwd_fp8_experts(x, None, rows, torch.tensor(off, dtype=torch.int32, device="cuda"), q, s, None, y)
+    assert (guard[:20] == 7.0).all() and (guard[29:] == 7.0).all()
+
+
+# ------------------------------------------------------------------------ norm
+
+def ops(K):
+    return K / 64 + 16
+
+
+@pytest.mark.parametrize("res", [None, F32, BF16])
+@pytest.mark.parametrize("out_dtype", [F32, BF16, E4])
+@pytest.mark.parametrize("M,K", [(1, 1), (3, 5), (4, 128), (6, 511), (5, 513), (1, 2048), (2100, 1030), (2049, 2048), (7, 2056),
+                                 (3, 4097), (2, 11008), (3, 12291), (2, 20001)])
+def test_norm(M, K, out_dtype, res):
+    x_dtype = BF16 if (M + K) % 2 else F32
+    x = make(M + K, M, K, dtype=x_dtype)
+    if M > 2:
+        x[1] = 0
+    r = None if res is None else make(M + K + 1, M, K, dtype=res)
+    if r is not None and M > 2:
+        r[1] = 0
+    w = None if M == 4 else 1 + 0.3 * make(K, K)
+    kept = None if r is None else torch.empty_like(r)
+    rstd = torch.empty(M, device="cuda")
+    out = torch.full((M, up(K, 128) if out_dtype == E4 else K), 1.0, device="cuda").to(out_dtype)
+    scales = torch.full((M, up(-(-K // 128), 4)), 255, dtype=torch.uint8, device="cuda").view(E8) if out_dtype == E4 else None
+    hx.hxq_rms_norm(x, w, 1e-5, out, scales=scales, residual=r, residual_out=kept, rstd=rstd)
+    h = x.cpu().float()
+    if r is not None:
+        h = (h + r.cpu().float()).to(res)
+        assert torch.equal(kept.cpu(), h)
+    Y, R = O.rms_norm(host(h), None if w is None else host(w), np.float64(np.float32(1e-5)))
+    tol = (ops(K) / 2 + 6) * U
+    near(rstd, R, tol * R, "rstd")
+    if out_dtype != E4:
+        near(out, Y, (tol + HALF[out_dtype]) * np.abs(Y), "norm")
+        return
+    # e4m3: half a step of 2^-4, or of the smallest value 2^-9; the scale by the rule, from a magnitude
+    # within the norm's tolerance
+    G = -(-K // 128)
+    S = raw(scales)
+    assert (S[:, G:] == 127).all()
+    top = np.pad(np.abs(Y), ((0, 0), (0, -K % 128))).reshape(M, G, 128).max(2)
+    assert ((S[:, :G] == O.scale_byte(top * (1 - tol))) | (S[:, :G] == O.scale_byte(top * (1 + tol)))).all()
+    got = O.wide_rows(raw(out), S)
+    assert (got[:, K:] == 0).all()
+    p = np.repeat(O.power(S[:, :G]), 128, axis=1)[:, :K]
+    assert (np.abs(got[:, :K] - Y) <= np.maximum(2.0**-4 * np.abs(Y) * (1 + 2 * tol), 2.0**-10 * p) + tol * np.abs(Y)).all()
+
+
+def test_norm_in_place_and_special_rows():
+    x, r = make(1, 6, 700), make(2, 6, 700, dtype=BF16)
+    x[1, 3], x[2, 4], x[3, 5] = float("nan"), float("inf"), 1e30  # (the last one's square overflows)
+    want, kept = torch.empty(6, 700, device="cuda"), torch.empty_like(r)
+    hx.hxq_rms_norm(x, None, 1e-6, want, residual=r, residual_out=kept)
+    r2, out = r.clone(), torch.empty_like(want)
+    hx.hxq_rms_norm(x, None, 1e-6, out, residual=r2, residual_out=r2)
+    assert torch.equal(r2.view(torch.int16), kept.view(torch.int16)) and torch.equal(out.view(torch.int32), want.view(torch.int32))
+    fine = torch.tensor([0, 4, 5])
+    Y, _ = O.rms_norm(host(kept)[fine], None, 1e-6)
+    near(want[fine], Y, (ops(700) / 2 + 6) * U * np.abs(Y))
+    assert want[1].isnan().all() and want[2, 4].isnan() and (want[3] == 0).all()
+
+
+@pytest.mark.parametrize("dres,dw", [(False, True), (True, True), (True, False)])
+@pytest.mark.parametrize("M,K", [(1, 1), (3, 7), (5, 512), (2100, 513), (4500, 130), (700, 2048), (3, 2056), (1500, 4096), (6, 11008), (5, 20001)])
+def test_norm_gradient(M, K, dres, dw):
+    h = make(M + K, M, K, dtype=BF16 if K % 2 else F32)
+    dy = make(M + K + 1, M, K, dtype=BF16 if M % 2 else F32)
+    w = None if M == 5 else 1 + 0.3 * make(K, K)
+    rstd = torch.from_numpy(O.rms_norm(host(h), None, 1e-6)[1]).float().cuda()
+    d = make(M + 7, M, K) if dres else None
+    dx, dweight = torch.full((M, K), float("nan"), device="cuda"), torch.full((K,), float("nan"), device="cuda") if dw else None
+    hx.hxq_rms_norm_bwd(dy, h, w, rstd, dx, dweight=dweight, dresidual=d)
+    H, D, W, R = host(h), host(dy), 1 if w is None else host(w), host(rstd)[:, None]
+    DX, DW = O.rms_norm_bwd(D, H, None if w is None else W, R[:, 0], None if d is None else host(d))
+    g = np.abs(D * W)
+    mean = (g * np.abs(H)).mean(1, keepdims=True)
+    bound = U * (8 * (R * g + R**3 * np.abs(H) * mean) + (ops(K) + 8) * R**3 * np.abs(H) * mean + 2 * np.abs(DX))
+    near(dx, DX, bound, "dx")
+    if dw:
+        near(dweight, DW, (min(M, 600) + 20) * U * (np.abs(D * H) * R).sum(0), "dweight")
+    if d is not None:  # dx over dresidual
+        again = torch.empty_like(dweight) if dw else None
+        hx.hxq_rms_norm_bwd(dy, h, w, rstd, d, dweight=again, dresidual=d)
+        assert torch.equal(d, dx) and (not dw or torch.equal(again, dweight))
+
+
+def test_norm_gradient_of_no_rows():
+    e = torch.empty((0, 9), device="cuda")
+    dw = torch.full((9,), 7.0, device="cuda")
+    hx.hxq_rms_norm_bwd(e, e, None, torch.empty(0, device="cuda"), e, dweight=dw)
+    assert not dw.any()
+    hx.hxq_rms_norm(e, None, 1e-6, e)
+
+
+# ---------------------------------------------------------------- layer objects
+
+def test_norm_under_autograd():
+    x, r = make(1, 2, 5, 300).requires_grad_(), make(2, 2, 5, 300, dtype=BF16).requires_grad_()
+    norm = hx.RmsNorm(1 + 0.2 * make(3, 300))
+    norm.weight.requires_grad_()
+    y, h = norm(x, r, out_dtype=F32)
+    dy, dh = make(4, 2, 5, 300), make(5, 2, 5, 300, dtype=BF16)
+    torch.autograd.backward((y, h), (dy, dh))
+    H = host(h).reshape(10, 300)
+    Y, R = O.rms_norm(H, host(norm.weight), 1e-6)
+    near(y.reshape(10, 300), Y, 20 * U * np.abs(Y))
+    DX, DW = O.rms_norm_bwd(host(dy).reshape(10, 300), H, host(norm.weight), R, host(dh).reshape(10, 300))
+    near(x.grad.reshape(10, 300), DX, 60 * U * np.abs(DX).max())
+    near(r.grad.reshape(10, 300), DX, 60 * U * np.abs(DX).max() + HALF[BF16] * np.abs(DX))
+    near(norm.weight.grad, DW, 60 * U * np.abs(DW).max())
+    assert x.grad.dtype == F32 and r.grad.dtype == BF16
+    # only one of the outputs used; no residual; frozen weight
+    x2 = make(1, 5, 300).requires_grad_()
+    _, h2 = norm(x2, make(2, 5, 300, dtype=BF16), out_dtype=F32)
+    h2.sum().backward()
+    assert torch.equal(x2.grad, torch.ones_like(x2))
+    x3 = make(1, 5, 300).requires_grad_()
+    frozen = hx.RmsNorm(None)
+    y3, none = frozen(x3, out_dtype=F32)
+    assert none is None
+    y3.backward(torch.ones_like(y3))
+    DX, _ = O.rms_norm_bwd(np.ones((5, 300)), host(x3), None, O.rms_norm(host(x3), None, 1e-6)[1])
+    near(x3.grad, DX, 60 * U * np.abs(DX).max())
+
+
+@pytest.mark.parametrize("M", [3, 200])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_linear_under_autograd(M, dtype):
+    N, K = 300, 200
+    w = make(2, N, K, scale=0.02)
+    layer = hx.Fp8Linear(w, make(3, N), train=True)
+    x = make(1, M, K, dtype=dtype).requires_grad_()
+    y = layer(x.reshape(1, M, K))
+    assert y.shape == (1, M, N) and y.dtype == F32
+    dy = make(4, M, N)
+    y.backward(dy[None])
+    Q, S = O.quant_weight(host(w))
+    W = O.wide_weight(Q, S)
+    D = O.wide_rows(*O.quant_rows(host(dy)))[:, :N]
+    DX, B = D @ W[:, :K], np.abs(D) @ np.abs(W[:, :K])
+    assert x.grad.dtype == dtype
+    near(x.grad, DX, 1e-5 * B + HALF[dtype] * np.abs(DX))
+    with pytest.raises(RuntimeError, match="train=True"):
+        hx.Fp8Linear(w)(x)
+
+
+def test_experts_under_autograd():
+    E, N, K, Mx = 5, 140, 260, 12
+    w = make(2, E, N, K, scale=0.02)
+    layer = hx.Fp8Experts(w, make(3, E, N), train=True)
+    rows, offsets = routing(1, [4, 0, 9, 2, 6], Mx, 3)
+    rows[21:] = -3
+    x = make(1, Mx, K).requires_grad_()
+    y = layer(x, offsets, rows)
+    assert (y[21:] == 0).all()
+    dy = make(4, 24, N)
+    dy[21:] = float("nan")  # gradients of rows that nothing computed
+    y.backward(dy)
+    D = O.wide_rows(*O.quant_rows(host(dy)[:21]))[:, :N]
+    each = [O.wide_weight(*O.quant_weight(host(w[e])))[:, :K] for e in range(E)]
+    DX, B = np.zeros((Mx, K)), np.zeros((Mx, K))
+    off, r = offsets.tolist(), rows.tolist()
+    for e in range(E):
+        for i in range(off[e], off[e + 1]):
+            DX[r[i]] += D[i] @ each[e]
+            B[r[i]] += np.abs(D[i]) @ np.abs(each[e])
+    near(x.grad, DX, 1e-5 * B)
+    x2 = make(1, 21, K).requires_grad_()
+    layer(x2, offsets).backward(dy[:21])
+    near(x2.grad[:4], D[:4] @ each[0], 1e-5 * (np.abs(D[:4]) @ np.abs(each[0])))
+
+
+@pytest.mark.parametrize("fmt", ["u8", "pk12"])
+def test_layers_from_compressed_ones(fmt):
+    """An 8-bit layer laid out from a compressed one holds its weight to half a step of e4m3."""
+    lays = [gen.random_layer(s, 200, 256, fmt, nnz=60, duplicates=True) for s in (1, 2)]
+    helix = [hx.HelixLinear.from_layer(l) for l in lays]
+    dense = [torch.empty((200, 256), dtype=BF16, device="cuda") for _ in helix]
+    for h, d in zip(helix, dense):
+        hx.hxq_dequant_bf16(hx.HXQ_FMT_U8 if fmt == "u8" else hx.HXQ_FMT_PK12, h.codebook, h.indices, h.sc_rows, h.sc_cols, h.sc_deltas, d)
+    x = make(1, 9, 256)
+    X = O.wide_rows(*O.quant_rows(host(x)))
+    for h, d in zip(helix, dense):
+        layer = hx.Fp8Linear.from_helix(h)
+        Y, B = O.linear(X, O.wide_weight(*O.quant_weight(host(d))), None if h.bias is None else host(h.bias))
+        near(layer(x), Y, 1e-5 * B + U * np.abs(Y))
+        assert layer.compressed_bytes() == 200 * 256 + 2 * 4
+    e = hx.Fp8Experts.from_helix(helix)
+    y = e(x, torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda"))
+    assert torch.equal(y[:4], hx.Fp8Linear.from_helix(helix[0])(x)[:4]) and torch.equal(y[4:], hx.Fp8Linear.from_helix(helix[1])(x)[4:])
+
+
+# ------------------------------------------------------------- as they are used
+
+def test_a_block_of_experts():
+    """norm -> experts -> gate -> experts -> norm, each fed by the one before, against the oracle fed with what
+    the GPU's step before it gave."""
+    T, K, F, E, top = 37, 256, 200, 6, 2
+    x, res = make(1, T, K), make(2, T, K, dtype=BF16)
+    norm = hx.RmsNorm(1 + 0.1 * make(3, K))
+    up_, down = hx.Fp8Experts(make(4, E, 2 * F, K, scale=0.05)), hx.Fp8Experts(make(5, E, K, F, scale=0.05))
+    chosen = torch.rand(T, E, generator=torch.Generator().manual_seed(6)).topk(top).indices.flatten()
+    order = chosen.sort(stable=True).indices
+    rows = (order // top).int().cuda()
+    offsets = torch.nn.functional.pad(torch.bincount(chosen, minlength=E).cumsum(0), (1, 0)).int().cuda()
+    (q, s), h = norm(x, res, out_dtype=E4)
+    a = up_((q, s), offsets, rows)
+    Y, B = O.experts(O.wide_rows(raw(q), raw(s)), rows.cpu().numpy(), offsets.tolist(),
+                     [O.wide_weight(raw(up_.wq[e]), raw(up_.w_scales[e])) for e in range(E)])
+    near(a, Y, 1e-5 * B)
+    g = (torch.nn.functional.silu(a[:, :F]) * a[:, F:]).contiguous()
+    d = down(g, offsets)
+    Y, B = O.experts(O.wide_rows(*O.quant_rows(host(g))), None, offsets.tolist(),
+                     [O.wide_weight(raw(down.wq[e]), raw(down.w_scales[e])) for e in range(E)])
+    near(d, Y, 1e-5 * B)
+    back = torch.empty(T * top, K, device="cuda")
+    back[order.cuda()] = d
+    out, h2 = norm(back.view(T, top, K).sum(1), h)
+    want = (back.view(T, top, K).sum(1).cpu() + h.cpu().float()).to(BF16)
+    assert torch.equal(h2.cpu(), want)
+    Y, _ = O.rms_norm(host(want), host(norm.weight), 1e-6)
+    near(out, Y, (20 * U + HALF[BF16]) * np.abs(Y))
+
+
+def test_captured_and_replayed():
+    """Norm and products in one graph, inputs changed between replays, eager work in between."""
+    T, K, N = 3, 512, 640
+    x, res, w = make(1, T, K), make(2, T, K, dtype=BF16), 1 + 0.1 * make(3, K)
+    layer = hx.Fp8Linear(make(4, N, K, scale=0.05))
+    many = make(8, 300, K, dtype=BF16)
+    experts = hx.Fp8Experts(make(5, 4, K, N, scale=0.05))
+    offsets = torch.tensor([0, 1, 1, 3, 3], dtype=torch.int32, device="cuda")
+    norm = hx.RmsNorm(w)
+
+    def step():
+        (q, s), h = norm(x, res, out_dtype=E4)
+        y = layer((q, s))
+        return y, h, experts(y, offsets), layer(many, out_dtype=BF16)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for i in range(4):
+        x.copy_(make(10 + i, T, K))
+        many.copy_(make(20 + i, 300, K, dtype=BF16))
+        offsets.copy_(torch.tensor([0, i % 3, i % 3, 2, 3], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        have = [t.clone() for t in got]
+        for a, b in zip(have, step()):
+            assert torch.equal(a, b)
+        torch.cuda.synchronize()
+
+
+def test_on_another_stream():
+    """Calls given a stream run there; two streams at once, each with a workspace of its own."""
+    N, K = 2048, 2048
+    q, s = weight8(make(1, N, K, scale=0.02))
+    xs = [make(i, 40, K, dtype=BF16) for i in range(2)]
+    want = [torch.empty((40, N), device="cuda") for _ in xs]
+    for x, y in zip(xs, want):
+        hx.hxq_linear_fwd_fp8(x, None, q, s, None, y)
+    got = [torch.empty_like(y) for y in want]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(20):
+        for x, y, st in zip(xs, got, streams):
+            hx.hxq_linear_fwd_fp8(x, None, q, s, None, y, stream=st)
+    for x, y, st in zip(xs, got, streams):
+        hx.hxq_linear_fwd_fp8(x, None, q, s, None, y, stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rows_past_32_bits():
+    """x of more than 2^32 bytes: the last rows are read where they are."""
+    M, K, N = 2**21 + 40, 2048, 40
+    x = torch.zeros((M, K), dtype=torch.uint8, device="cuda").view(E4)
+    s = torch.full((M, 4), 127, dtype=torch.uint8, device="cuda").view(E8)
+    last = make(1, 40, K)
+    lq, ls = rows8(last)
+    x.view(torch.uint8)[-40:] = lq.view(torch.uint8)
+    s = torch.full((M, 16), 127, dtype=torch.uint8, device="cuda")
+    s[-40:] = ls.view(torch.uint8)
+    q, ws = weight8(make(2, N, K, scale=0.02))
+    y = torch.empty((M, N), device="cuda")
+    hx.hxq_linear_fwd_fp8(x, s.view(E8), q, ws, None, y)
+    Y, B = O.linear(O.wide_rows(raw(lq), raw(ls)), O.wide_weight(raw(q), raw(ws)))
+    near(y[-40:], Y, 1e-5 * B)
+    assert not y[:-40].any()
+    rows = torch.arange(M - 40, M, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    ye = torch.empty((40, N), device="cuda")
+    hx.hxq_linear_fwd_fp8_experts(x, s.view(E8), rows, torch.tensor([0, 40], dtype=torch.int32, device="cuda"), q[None], ws[None], None, ye)
+    near(ye.flip(0), Y, 1e-5 * B)

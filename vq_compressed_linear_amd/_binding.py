@@ -32,6 +32,7 @@ HXQ_SCRATCH_BYTES = 96 * 1024 * 1024
 
 HXQ_F32 = 0
 HXQ_BF16 = 1
+HXQ_E4M3 = 2
 
 HXQ_VARIANT_AUTO = 0
 HXQ_VARIANT_GEMV_VALU = 1
@@ -106,6 +107,16 @@ SIGNATURES = {
                                         _P]),
     "hxq_linear_bwd_x_grouped_workspace": (_I64, [_INT, _INT, ctypes.POINTER(HxqBwdLayer), _INT, _I64, _I64]),
     "hxq_select_variant": (_INT, [_INT, _INT, _I64, _I64, _I64]),
+    "hxq_quant_fp8": (_INT, [_P, _INT, _P, _P, _I64, _I64, _P]),
+    "hxq_quant_fp8_weight": (_INT, [_P, _INT, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "hxq_linear_fwd_fp8": (_INT, [_P, _INT, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _P, _I64, _P]),
+    "hxq_linear_fwd_fp8_workspace": (_I64, [_INT, _I64, _I64, _I64]),
+    "hxq_linear_fwd_fp8_experts": (_INT, [_P, _INT, _P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64,
+                                          _P, _I64, _P]),
+    "hxq_linear_fwd_fp8_experts_workspace": (_I64, [_INT, _I64, _I64, _I64, _I64, _I64]),
+    "hxq_rms_norm": (_INT, [_P, _INT, _P, _INT, _P, ctypes.c_float, _P, _P, _INT, _P, _P, _I64, _I64, _P]),
+    "hxq_rms_norm_bwd": (_INT, [_P, _INT, _P, _INT, _P, _P, _P, _P, _P, _I64, _I64, _P, _I64, _P]),
+    "hxq_rms_norm_bwd_workspace": (_I64, [_I64, _I64]),
     "hxq_status_str": (ctypes.c_char_p, [_INT]),
     "hxq_version": (_INT, []),
     "hxq_source_digest": (ctypes.c_char_p, []),

@@ -826,7 +826,7 @@ const char* hxq_status_str(int status) {
   }
 }
 
-int hxq_version(void) { return 100; }
+int hxq_version(void) { return 200; }
 
 #ifndef HXQ_SOURCE_DIGEST
 #define HXQ_SOURCE_DIGEST "unknown"
