@@ -85,6 +85,7 @@ struct Fp8Plan {
 enum Fp8Kernel { kFp8Skinny16 = 0, kFp8Skinny32 = 1, kFp8Skinny64 = 2, kFp8Tile256 = 3 };
 
 hipError_t launch_fp8_skinny(const Fp8Args& a, const Fp8Plan& p, hipStream_t stream);
+hipError_t launch_fp8_tile256(const Fp8Args& a, const Fp8Plan& p, hipStream_t stream);
 hipError_t launch_fp8_sum(const Fp8Args& a, hipStream_t stream);
 
 }  // namespace hxq

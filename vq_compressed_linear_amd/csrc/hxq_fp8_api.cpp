@@ -34,20 +34,24 @@ T* at(T* p, int64_t bytes) {
 const void* at(const void* p, int64_t bytes) { return p ? static_cast<const char*>(p) + bytes : nullptr; }
 void* at(void* p, int64_t bytes) { return p ? static_cast<char*>(p) + bytes : nullptr; }
 
-// Which kernel runs a product over `M` rows of y (of `E` experts), and how its
-// sum over k is split.
-hxq::Fp8Plan plan(int64_t M, int64_t N, int64_t K, int64_t E) {
+// Which kernel runs a product over `M` rows of y (of `E` experts; `gather`:
+// rows of x by index), and how its sum over k is split.
+hxq::Fp8Plan plan(int64_t Mx, int64_t M, int64_t N, int64_t K, int64_t E, bool gather) {
   hxq::Fp8Plan p = {};
-  const int64_t blocks = fp8_padded(K) / 128, cus = hxq::device_cu_count();
+  const int64_t Kp = fp8_padded(K), blocks = Kp / 128, cus = hxq::device_cu_count();
   const int64_t each = (M + E - 1) / E;  // rows of an expert, if they were even
-  p.kernel = each <= 16 ? hxq::kFp8Skinny16 : each <= 32 ? hxq::kFp8Skinny32 : hxq::kFp8Skinny64;
-  const int64_t tm = each <= 16 ? 16 : each <= 32 ? 32 : 64, tn = tm;
+  // the tile kernel's offsets within a tile's operands (or a gathered x) are 32 bits
+  const bool near32 = K > 0 && (gather ? Mx : 256) * Kp < ((int64_t)1 << 32) && Kp < ((int64_t)1 << 24);
+  p.kernel = each <= 16 ? hxq::kFp8Skinny16 : each <= 32 ? hxq::kFp8Skinny32 : each <= 64 || !near32 ? hxq::kFp8Skinny64 : hxq::kFp8Tile256;
+  const int64_t tm = p.kernel == hxq::kFp8Skinny16 ? 16 : p.kernel == hxq::kFp8Skinny32 ? 32 : p.kernel == hxq::kFp8Skinny64 ? 64 : 256;
+  const int64_t tn = tm;
   p.waves = p.kernel == hxq::kFp8Skinny16 && blocks >= 32 ? 8 : 4;
   p.tiles_n = (N + tn - 1) / tn;
   p.tiles_m = E > 1 ? M / tm + std::min(E, M) : (M + tm - 1) / tm;
   p.S = 1;
   const int64_t wgs = p.tiles_n * p.tiles_m;
-  if (wgs < cus && blocks >= 4 * p.waves) p.S = (int)std::min<int64_t>((2 * cus + wgs - 1) / wgs, blocks / (2 * p.waves));
+  if (p.kernel != hxq::kFp8Tile256 && wgs < cus && blocks >= 4 * p.waves)
+    p.S = (int)std::min<int64_t>((2 * cus + wgs - 1) / wgs, blocks / (2 * p.waves));
   p.kbs = (int)((blocks + p.S - 1) / p.S);
   if (p.kbs > 0) p.S = (int)((blocks + p.kbs - 1) / p.kbs);
   if (p.S < 1) p.S = 1;
@@ -92,7 +96,7 @@ int product(const void* x, int x_dtype, const uint8_t* x_scales, const int32_t* 
     return HXQ_ERR_SHAPE;
   if (M == 0 || N == 0) return HXQ_OK;
   if (Mx == 0) return HXQ_ERR_SHAPE;
-  const hxq::Fp8Plan p = plan(M, N, K, E);
+  const hxq::Fp8Plan p = plan(Mx, M, N, K, E, rows != nullptr);
   if (!p.ok) return HXQ_ERR_SHAPE;
   if (!y) return HXQ_ERR_NULL;
   if (K > 0 && (!x || !wq || !w_scales || (x_dtype == HXQ_E4M3 && !x_scales))) return HXQ_ERR_NULL;
@@ -130,7 +134,7 @@ int product(const void* x, int x_dtype, const uint8_t* x_scales, const int32_t* 
     const hipError_t e = quant_rows(x, x_dtype, ws + w.xq, ws + w.xs, Mx, K, stream);
     if (e != hipSuccess) return HXQ_ERR_HIP;
   }
-  hipError_t e = hxq::launch_fp8_skinny(a, p, stream);
+  hipError_t e = p.kernel == hxq::kFp8Tile256 ? hxq::launch_fp8_tile256(a, p, stream) : hxq::launch_fp8_skinny(a, p, stream);
   if (e == hipSuccess && p.S > 1) e = hxq::launch_fp8_sum(a, stream);
   return status_of(e);
 }
@@ -139,7 +143,7 @@ int64_t product_workspace(int x_dtype, int64_t Mx, int64_t M, int64_t E, int64_t
   if (!float_dtype(x_dtype) && x_dtype != HXQ_E4M3) return HXQ_ERR_DTYPE;
   if (bad_dim(Mx) || bad_dim(M) || bad_dim(N) || bad_dim(K) || E < 1 || E > kMaxExperts) return HXQ_ERR_SHAPE;
   if (M == 0 || N == 0) return 0;
-  const hxq::Fp8Plan p = plan(M, N, K, E);
+  const hxq::Fp8Plan p = plan(Mx, M, N, K, E, true);
   if (!p.ok || Mx == 0) return HXQ_ERR_SHAPE;
   return workspace_of(p, x_dtype, Mx, K).bytes;
 }

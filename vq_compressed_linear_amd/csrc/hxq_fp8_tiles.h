@@ -51,6 +51,13 @@ __device__ __forceinline__ RowTile fp8_row_tile(const Fp8Args& a, int t, int tm)
   return {0, 0, 0};
 }
 
+// How many such tiles there are.
+__device__ __forceinline__ int fp8_row_tiles(const Fp8Args& a, int tm) {
+  int n = 0;
+  for (int e = lane_id(); e < a.E; e += kWave) n += (int)(((int64_t)max(fp8_offset(a, e + 1) - fp8_offset(a, e), 0) + tm - 1) / tm);
+  return wave_sum_dpp_i(n);
+}
+
 // The expert of row m (m < fp8_rows_end): the last e with offset(e) <= m.
 __device__ __forceinline__ int fp8_expert_of(const Fp8Args& a, int m) {
   int lo = 0, hi = a.E;  // offset(lo) <= m < offset(hi)
