@@ -76,16 +76,17 @@ struct Fp8Args {
 // How a product is run (host): which kernel, and how its sum is split.
 struct Fp8Plan {
   int kernel;       // one of Fp8Kernel
+  bool wide;        // operands widened to bf16 (tile kernels)
   int waves;        // waves that share a tile's sum (skinny kernels)
   int S, kbs;
   int64_t tiles_m, tiles_n;
   int64_t part_bytes;
   bool ok;          // the tiles can be numbered in 31 bits
 };
-enum Fp8Kernel { kFp8Skinny16 = 0, kFp8Skinny32 = 1, kFp8Skinny64 = 2, kFp8Tile256 = 3 };
+enum Fp8Kernel { kFp8Skinny, kFp8Tile32, kFp8Tile64, kFp8Tile128, kFp8Tile256 };
 
 hipError_t launch_fp8_skinny(const Fp8Args& a, const Fp8Plan& p, hipStream_t stream);
-hipError_t launch_fp8_tile256(const Fp8Args& a, const Fp8Plan& p, hipStream_t stream);
+hipError_t launch_fp8_tile(const Fp8Args& a, const Fp8Plan& p, hipStream_t stream);
 hipError_t launch_fp8_sum(const Fp8Args& a, hipStream_t stream);
 
 }  // namespace hxq

@@ -34,25 +34,50 @@ T* at(T* p, int64_t bytes) {
 const void* at(const void* p, int64_t bytes) { return p ? static_cast<const char*>(p) + bytes : nullptr; }
 void* at(void* p, int64_t bytes) { return p ? static_cast<char*>(p) + bytes : nullptr; }
 
+// Rows of x and outputs of a workgroup's tile, by kernel.
+constexpr int64_t kTileRows[] = {16, 32, 64, 128, 256};
+constexpr int64_t kTileOutputs[] = {16, 64, 128, 128, 256};
+
 // Which kernel runs a product over `M` rows of y (of `E` experts; `gather`:
 // rows of x by index), and how its sum over k is split.
-hxq::Fp8Plan plan(int64_t Mx, int64_t M, int64_t N, int64_t K, int64_t E, bool gather) {
+hxq::Fp8Plan plan(bool y_bf16, int64_t Mx, int64_t M, int64_t N, int64_t K, int64_t E, bool gather) {
   hxq::Fp8Plan p = {};
   const int64_t Kp = fp8_padded(K), blocks = Kp / 128, cus = hxq::device_cu_count();
   const int64_t each = (M + E - 1) / E;  // rows of an expert, if they were even
-  // the tile kernel's offsets within a tile's operands (or a gathered x) are 32 bits
+  p.wide = !y_bf16;
+  auto tiles_m = [&](int k) {
+    const int64_t tm = kTileRows[k];
+    return E > 1 ? M / tm + std::min(E, M) : (M + tm - 1) / tm;
+  };
+  auto tiles = [&](int k) { return tiles_m(k) * ((N + kTileOutputs[k] - 1) / kTileOutputs[k]); };
+  // workgroups that share a tile's sum: to fill the CUs, each with at least 12 blocks
+  auto splits = [&](int k) {
+    if (k > hxq::kFp8Tile64) return (int64_t)1;
+    return std::max<int64_t>(1, std::min(cus / std::max<int64_t>(1, tiles(k)), blocks / 12));
+  };
+  auto fills = [&](int k) { return 10 * tiles(k) * splits(k) >= 6 * cus; };
   const bool near32 = K > 0 && (gather ? Mx : 256) * Kp < ((int64_t)1 << 32) && Kp < ((int64_t)1 << 24);
-  p.kernel = each <= 16 ? hxq::kFp8Skinny16 : each <= 32 ? hxq::kFp8Skinny32 : each <= 64 || !near32 ? hxq::kFp8Skinny64 : hxq::kFp8Tile256;
-  const int64_t tm = p.kernel == hxq::kFp8Skinny16 ? 16 : p.kernel == hxq::kFp8Skinny32 ? 32 : p.kernel == hxq::kFp8Skinny64 ? 64 : 256;
-  const int64_t tn = tm;
-  p.waves = p.kernel == hxq::kFp8Skinny16 && blocks >= 32 ? 8 : 4;
-  p.tiles_n = (N + tn - 1) / tn;
-  p.tiles_m = E > 1 ? M / tm + std::min(E, M) : (M + tm - 1) / tm;
-  p.S = 1;
+  if (!near32 || each <= (E > 1 ? 1 : 8) || (each <= 128 && tiles(hxq::kFp8Skinny) * blocks <= 32 * cus))
+    p.kernel = hxq::kFp8Skinny;
+  else if (each >= 192 && fills(hxq::kFp8Tile256))
+    p.kernel = hxq::kFp8Tile256;
+  else if (p.wide && each >= 96 && fills(hxq::kFp8Tile128))
+    p.kernel = hxq::kFp8Tile128;
+  else if (each >= (E > 1 ? 6 : 33) && fills(hxq::kFp8Tile64))
+    p.kernel = hxq::kFp8Tile64;
+  else
+    p.kernel = hxq::kFp8Tile32;
+  const bool skinny = p.kernel == hxq::kFp8Skinny;
+  p.waves = blocks >= 32 ? 8 : 4;
+  p.tiles_n = (N + kTileOutputs[p.kernel] - 1) / kTileOutputs[p.kernel];
+  p.tiles_m = tiles_m(p.kernel);
   const int64_t wgs = p.tiles_n * p.tiles_m;
-  if (p.kernel != hxq::kFp8Tile256 && wgs < cus && blocks >= 4 * p.waves)
-    p.S = (int)std::min<int64_t>((2 * cus + wgs - 1) / wgs, blocks / (2 * p.waves));
+  if (skinny)
+    p.S = wgs < cus && blocks >= 4 * p.waves ? (int)std::min<int64_t>((2 * cus + wgs - 1) / wgs, blocks / (2 * p.waves)) : 1;
+  else
+    p.S = (int)splits(p.kernel);
   p.kbs = (int)((blocks + p.S - 1) / p.S);
+  if (p.S > 1 && !skinny) p.kbs = (p.kbs + 3) / 4 * 4;  // whole words of scales
   if (p.kbs > 0) p.S = (int)((blocks + p.kbs - 1) / p.kbs);
   if (p.S < 1) p.S = 1;
   p.ok = p.tiles_n <= kMaxTiles && p.tiles_m <= kMaxTiles && p.tiles_n * p.tiles_m * p.S <= kMaxTiles;
@@ -96,7 +121,7 @@ int product(const void* x, int x_dtype, const uint8_t* x_scales, const int32_t* 
     return HXQ_ERR_SHAPE;
   if (M == 0 || N == 0) return HXQ_OK;
   if (Mx == 0) return HXQ_ERR_SHAPE;
-  const hxq::Fp8Plan p = plan(Mx, M, N, K, E, rows != nullptr);
+  const hxq::Fp8Plan p = plan(y_dtype == HXQ_BF16, Mx, M, N, K, E, rows != nullptr);
   if (!p.ok) return HXQ_ERR_SHAPE;
   if (!y) return HXQ_ERR_NULL;
   if (K > 0 && (!x || !wq || !w_scales || (x_dtype == HXQ_E4M3 && !x_scales))) return HXQ_ERR_NULL;
@@ -134,7 +159,7 @@ int product(const void* x, int x_dtype, const uint8_t* x_scales, const int32_t* 
     const hipError_t e = quant_rows(x, x_dtype, ws + w.xq, ws + w.xs, Mx, K, stream);
     if (e != hipSuccess) return HXQ_ERR_HIP;
   }
-  hipError_t e = p.kernel == hxq::kFp8Tile256 ? hxq::launch_fp8_tile256(a, p, stream) : hxq::launch_fp8_skinny(a, p, stream);
+  hipError_t e = p.kernel == hxq::kFp8Skinny ? hxq::launch_fp8_skinny(a, p, stream) : hxq::launch_fp8_tile(a, p, stream);
   if (e == hipSuccess && p.S > 1) e = hxq::launch_fp8_sum(a, stream);
   return status_of(e);
 }
@@ -143,7 +168,7 @@ int64_t product_workspace(int x_dtype, int64_t Mx, int64_t M, int64_t E, int64_t
   if (!float_dtype(x_dtype) && x_dtype != HXQ_E4M3) return HXQ_ERR_DTYPE;
   if (bad_dim(Mx) || bad_dim(M) || bad_dim(N) || bad_dim(K) || E < 1 || E > kMaxExperts) return HXQ_ERR_SHAPE;
   if (M == 0 || N == 0) return 0;
-  const hxq::Fp8Plan p = plan(Mx, M, N, K, E, true);
+  const hxq::Fp8Plan p = plan(false, Mx, M, N, K, E, true);
   if (!p.ok || Mx == 0) return HXQ_ERR_SHAPE;
   return workspace_of(p, x_dtype, Mx, K).bytes;
 }

@@ -41,83 +41,125 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int TILE = 256, ROW = 128, STAGE = 2 * TILE * ROW;
+constexpr int ROW = 128;  // bytes of a row in a stage
 
-// 64 lanes x 16 bytes, from base + off (of each lane) to the 1024 bytes of LDS at `lds`.
+// 64 lanes x 16 (4) bytes, from base + off (of each lane) to the 1024 (256) bytes of LDS at `lds`.
 __device__ __forceinline__ void request_lines(const uint8_t* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(lds), "v"(off), "s"(base)
                : "memory", "m0");
 }
+__device__ __forceinline__ void request_words(const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
 
-template <bool WIDE>
-__global__ __launch_bounds__(512, 2) void fp8_tile256(Fp8Args a, int tiles_n, int tiles_m) {
-  __shared__ __align__(1024) uint8_t lds[2 * STAGE];
+// WM x WN waves, each FJ blocks of 32 rows of x by FI blocks of 32 outputs; SLOTS stages in LDS.
+template <int WM, int WN, int FJ, int FI, int SLOTS>
+struct TileShape {
+  static constexpr int WAVES = WM * WN, TM = 32 * WM * FJ, TN = 32 * WN * FI;
+  static constexpr int STAGE = (TM + TN) * ROW;
+  static constexpr int PER = (TM + TN) / 8 / WAVES;  // line requests of a wave and stage
+  static constexpr int XWORDS = TM < 64 ? 64 : TM;   // a group's scale words: x's rows, then the weight's blocks
+  static constexpr int WORDS = 4 * (XWORDS + 64);
+  static constexpr int WPER = (XWORDS / 64 + WAVES) / WAVES;  // word requests of a wave and group
+  static constexpr int LDS = SLOTS * STAGE + 2 * WORDS;
+  static_assert(PER * 8 * WAVES == TM + TN && SLOTS <= 4 && LDS <= 160 * 1024, "tile shape");
+};
+
+template <bool WIDE, int WM, int WN, int FJ, int FI, int SLOTS>
+__global__ __launch_bounds__(64 * WM * WN, FI * FJ > 8 ? 1 : 2) void fp8_tile(Fp8Args a, int tiles_n, int tiles_m) {
+  using T = TileShape<WM, WN, FJ, FI, SLOTS>;
+  constexpr int TM = T::TM, TN = T::TN, STAGE = T::STAGE, PER = T::PER;
+  __shared__ __align__(1024) uint8_t lds[T::LDS];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 1, wn = wave >> 1;  // 2 x 4 over the tile
+  const int wm = wave % WM, wn = wave / WM;
   const int r32 = lane & 31, half = lane >> 5;
 
   // tiles of eight row tiles (all of a column of them first) stay together on
   // one XCD, which then shares their lines in its L2
-  const int total_m = a.offsets ? fp8_row_tiles(a, TILE) : tiles_m;
-  const int64_t work = (int64_t)total_m * tiles_n;
+  const int total_m = a.offsets ? fp8_row_tiles(a, TM) : tiles_m;
+  const int64_t work = (int64_t)total_m * tiles_n * a.S;
   if ((int64_t)blockIdx.x >= work) return;
   const int per = (int)(work >> 3);
   const int bx = blockIdx.x;
-  const int L = bx < 8 * per ? (bx & 7) * per + (bx >> 3) : bx;
+  int L = bx < 8 * per ? (bx & 7) * per + (bx >> 3) : bx;
+  const int split = L / (total_m * tiles_n);
+  L -= split * (total_m * tiles_n);
   const int group = L / (8 * tiles_n), in = L - group * 8 * tiles_n;
   const int gm = min(8, total_m - 8 * group);
   const int tn = in / gm, tm = 8 * group + in - tn * gm;
-  const RowTile t = fp8_row_tile(a, tm, TILE);
+  const RowTile t = fp8_row_tile(a, tm, TM);
   if (t.rows <= 0) return;
-  const int n0 = tn * TILE;
-  const int nk = a.Kp >> 7, nb = (a.N + 127) >> 7;
+  const int n0 = tn * TN;
+  const int nb = (a.N + 127) >> 7;
+  const int kb0 = split * a.kbs, nk = min(a.kbs, (a.Kp >> 7) - kb0);  // the split's stages (kbs % 4 == 0 if split)
 
-  // this wave's lines of a stage: rows 32 wave .. + 31 of x and of the weight
+  // this wave's lines of a stage: of the tile's rows of x, then of the weight
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  const uint8_t* wbase = a.w + ((int64_t)t.expert * a.N + n0) * a.Kp;
-  const uint8_t* xbase = a.rows ? a.x : a.x + (int64_t)t.row0 * a.Kp;
-  uint32_t xoff[4], woff[4];
+  const uint8_t* wbase = a.w + ((int64_t)t.expert * a.N + n0) * a.Kp + (int64_t)kb0 * ROW;
+  const uint8_t* xbase = (a.rows ? a.x : a.x + (int64_t)t.row0 * a.Kp) + (int64_t)kb0 * ROW;
+  const uint8_t* line_base[PER];
+  uint32_t line_off[PER];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = 32 * wave + 8 * j + (lane >> 3);
+  for (int j = 0; j < PER; ++j) {
+    const int r = 8 * (PER * wave + j) + (lane >> 3);
+    const bool of_x = 8 * (PER * wave + j) < TM;
     const uint32_t piece = (uint32_t)((lane & 7) ^ ((r >> 1) & 7)) << 4;
     const int m = min(r, t.rows - 1);
-    xoff[j] = (uint32_t)(a.rows ? fp8_x_row(a, t.row0 + m) : m) * (uint32_t)a.Kp + piece;
-    woff[j] = (uint32_t)min(r, a.N - 1 - n0) * (uint32_t)a.Kp + piece;
+    const uint32_t row = of_x ? (uint32_t)(a.rows ? fp8_x_row(a, t.row0 + m) : m) : (uint32_t)min(r - TM, a.N - 1 - n0);
+    line_off[j] = row * (uint32_t)a.Kp + piece;
+    line_base[j] = of_x ? xbase : wbase;
   }
-  auto request = [&](int s) {
-    const uint32_t d = lds0 + (s & 1) * STAGE + wave * (32 * ROW);
+  // and scale words (four stages' bytes), a wave's 64 of them: x's rows, then the weight's blocks (which the
+  // waves left over request as well: a branch here would part the matrix ops around it)
+  const uint8_t* word_base[T::WPER];
+  uint32_t word_off[T::WPER], word_to[T::WPER];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) request_lines(xbase + (int64_t)s * ROW, xoff[j], d + j * (8 * ROW));
+  for (int j = 0; j < T::WPER; ++j) {
+    const int w = min(wave + j * T::WAVES, T::XWORDS / 64);
+    word_to[j] = lds0 + SLOTS * STAGE + 256 * w;
+    if (w < T::XWORDS / 64) {
+      const int m = min(64 * w + lane, t.rows - 1);
+      word_base[j] = (a.rows ? a.xs : a.xs + (int64_t)t.row0 * a.Gs) + kb0;
+      word_off[j] = (uint32_t)(a.rows ? fp8_x_row(a, t.row0 + m) : m) * (uint32_t)a.Gs;
+    } else {
+      word_base[j] = a.ws + ((int64_t)t.expert * nb + (n0 >> 7)) * a.Gs + kb0;
+      word_off[j] = (uint32_t)min(lane, nb - 1 - (n0 >> 7)) * (uint32_t)a.Gs;
+    }
+  }
+  const uint32_t words0 = lds0 + SLOTS * STAGE;
+  auto request = [&](auto words, int s, uint32_t slot) {
+    if constexpr (decltype(words)::value)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) request_lines(wbase + (int64_t)s * ROW, woff[j], d + TILE * ROW + j * (8 * ROW));
+      for (int j = 0; j < T::WPER; ++j)
+        request_words(word_base[j] + (s & ~3), word_off[j], word_to[j] + ((s >> 2) & 1) * T::WORDS);
+    const uint32_t d = lds0 + slot * STAGE + wave * (PER * 1024);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) request_lines(line_base[j] + (int64_t)s * ROW, line_off[j], d + j * 1024);
   };
 
-  // scales: a word holds four stages' bytes
-  const uint8_t* wsp = a.ws + ((int64_t)t.expert * nb + min((n0 + 64 * wn) >> 7, nb - 1)) * a.Gs;
-  const uint8_t* xsp[4];
+  uint32_t sw, sx[FJ], sw_next, sx_next[FJ];
+  auto read_scales = [&](int s) {  // the words of the group of stage s
+    typedef __attribute__((address_space(3))) const uint32_t lds_word;
+    const uint32_t o = words0 + ((s >> 2) & 1) * T::WORDS;
+    sw_next = *(lds_word*)(o + 4 * T::XWORDS + 4 * ((32 * FI * wn) >> 7));
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    xsp[j] = a.xs + fp8_x_row(a, t.row0 + min(128 * wm + 32 * j + r32, t.rows - 1)) * a.Gs;
-  uint32_t sw, sx[4], sw_next, sx_next[4];
-  auto load_scales = [&](int s) {  // of stages s .. s + 3 (s % 4 == 0)
-    const int at = min(s, a.Gs - 4);
-    sw_next = *reinterpret_cast<const uint32_t*>(wsp + at);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sx_next[j] = *reinterpret_cast<const uint32_t*>(xsp[j] + at);
+    for (int j = 0; j < FJ; ++j) sx_next[j] = *(lds_word*)(o + 4 * (32 * (FJ * wm + j) + r32));
   };
 
   // operand reads: piece 4 k64 + 2 half + q of row r32 (q = 0, 1), rows 32 apart 4096 bytes apart
   const int swz = (r32 >> 1) & 7;
   const uint32_t rd = lds0 + r32 * ROW + (((2 * half) ^ swz) << 4);
-  const uint32_t rx = rd + 128 * wm * ROW, rw = rd + TILE * ROW + 64 * wn * ROW;
-  // where the reads of (stage s, k64) start (piece q at + 16 q, flipped: the bit is never carried); kept
+  const uint32_t rx = rd + 32 * FJ * wm * ROW, rw = rd + TM * ROW + 32 * FI * wn * ROW;
+  // where the reads of (slot, k64) start (piece q at + 16 q, flipped: the bit is never carried); kept
   // from being computed for all of a loop's stages ahead, which would not fit the registers
-  auto at = [&](uint32_t base, int s, int k64) {
-    uint32_t o = (base ^ (uint32_t)(k64 << 6)) + (s & 1) * STAGE;
+  auto at = [&](uint32_t base, uint32_t slot, int k64) {
+    uint32_t o = (base ^ (uint32_t)(k64 << 6)) + slot * STAGE;
     asm volatile("" : "+v"(o));
     return o;
   };
@@ -126,31 +168,31 @@ __global__ __launch_bounds__(512, 2) void fp8_tile256(Fp8Args a, int tiles_n, in
     const i32x4 lo = *(lds_vec*)(o + row * ROW), hi = *(lds_vec*)((o ^ 16) + row * ROW);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  i32x8 wcur[2], wnext[2], x[4];  // 32 bytes of a row each; x is read again as soon as its last matrix op is issued
+  i32x8 wcur[FI], wnext[FI], x[FJ];  // 32 bytes of a row each; x is read again as soon as its last matrix op is issued
 
-  f32x16 acc[2][4];
+  f32x16 acc[FI][FJ];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < FI; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < FJ; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-  // the matrix ops of one 64 of k, each x block's next bytes read behind them
+  // the matrix ops of one 64 of k, each x block's next bytes (of slot, k64) read behind them
   // (past the last stage what the slot holds, which nothing uses); SEL: the
   // stage's byte of the scale words
-  auto step = [&](auto sel, int s, int k64) {
+  auto step = [&](auto sel, uint32_t slot, int k64) {
     constexpr int SEL = decltype(sel)::value;
     const float fw = __uint_as_float(((sw >> (8 * SEL)) & 255u) << 23);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) wcur[i] = wnext[i];
-    const uint32_t ow = at(rw, s, k64), ox = at(rx, s, k64);
+    for (int i = 0; i < FI; ++i) wcur[i] = wnext[i];
+    const uint32_t ow = at(rw, slot, k64), ox = at(rx, slot, k64);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) wnext[i] = read32(ow, 32 * i);
+    for (int i = 0; i < FI; ++i) wnext[i] = read32(ow, 32 * i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < FJ; ++j) {
       if constexpr (!WIDE) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < FI; ++i)
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wcur[i], x[j], acc[i][j], 0, 0, SEL, (int)sw, SEL,
                                                                      (int)sx[j]);
       } else {
@@ -159,7 +201,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile256(Fp8Args a, int tiles_n, in
         for (int p = 0; p < 4; ++p) {  // 8 bytes of each lane: 16 of the 64 k
           const bf16x8 xv = widen8(x[j][2 * p], x[j][2 * p + 1], fx);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < FI; ++i)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8(wcur[i][2 * p], wcur[i][2 * p + 1], fw), xv,
                                                                acc[i][j], 0, 0, 0);
         }
@@ -168,110 +210,171 @@ __global__ __launch_bounds__(512, 2) void fp8_tile256(Fp8Args a, int tiles_n, in
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto landed = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); };
-
-  auto take_scales = [&]() {
-    sw = sw_next;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sx[j] = sx_next[j];
-  };
-  // a stage; REQ: stage s + 2 is there
-  auto stage = [&](auto sel, auto req, int s) {
-    step(sel, s, 1);
-    landed();
-    __builtin_amdgcn_s_barrier();
-    // (the words requested in the group's first stage are here: looked at now, the compiler's wait for them is free)
-    if constexpr (decltype(sel)::value == 1)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(sx_next[j]));
-    if constexpr (decltype(req)::value) request(s + 2);
-    step(sel, s + 1, 0);
+  // all but the newest LEFT requests of this wave have landed, and its reads of LDS are back
+  auto landed = [&](auto left) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(left)::value) : "memory");
   };
   using std::integral_constant;
   constexpr integral_constant<int, 0> s0{};
   constexpr integral_constant<int, 1> s1{};
   constexpr integral_constant<int, 2> s2{};
   constexpr integral_constant<int, 3> s3{};
+  constexpr integral_constant<int, (SLOTS - 2) * PER> behind{};
+  auto next = [](uint32_t slot) { return slot + 1 == SLOTS ? 0u : slot + 1; };
+  // stage s, in `slot`; req: stage s + SLOTS is there (and so are the ones before it); words: its scale words too
+  auto stage = [&](auto sel, auto req, auto words, int s, uint32_t slot) {
+    step(sel, slot, 1);
+    if constexpr (decltype(req)::value)
+      landed(behind);
+    else
+      landed(s0);
+    __builtin_amdgcn_s_barrier();
+    if constexpr (decltype(req)::value) request(words, s + SLOTS, slot);
+    step(sel, next(slot), 0);
+  };
+  auto take_scales = [&]() {
+    sw = sw_next;
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) sx[j] = sx_next[j];
+  };
 
-  request(0);
-  load_scales(0);
-  landed();
+  request(std::true_type{}, 0, 0);
+  landed(s0);
   __builtin_amdgcn_s_barrier();
-  if (nk > 1) request(1);
+#pragma unroll
+  for (int i = 1; i < SLOTS; ++i)
+    if (nk > i) request(std::false_type{}, i, i);
+  read_scales(0);
   take_scales();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) wnext[i] = read32(rw, 32 * i);
+  for (int i = 0; i < FI; ++i) wnext[i] = read32(rw, 32 * i);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) x[j] = read32(rx, 32 * j);
-  // four stages to a scale word while there are two more behind them, then the rest
+  for (int j = 0; j < FJ; ++j) x[j] = read32(rx, 32 * j);
+  // four stages to a scale word while all four have stage s + SLOTS, then the rest
   int s = 0;
-  for (; s + 6 <= nk; s += 4) {
-    load_scales(s + 4);
-    stage(s0, std::true_type{}, s);
-    stage(s1, std::true_type{}, s + 1);
-    stage(s2, std::true_type{}, s + 2);
-    stage(s3, std::true_type{}, s + 3);
+  uint32_t slot = 0;
+  for (; s + 4 + SLOTS <= nk; s += 4) {
+    stage(s0, std::true_type{}, integral_constant<bool, (SLOTS + 0) % 4 == 0>{}, s, slot);
+    slot = next(slot);
+    stage(s1, std::true_type{}, integral_constant<bool, (SLOTS + 1) % 4 == 0>{}, s + 1, slot);
+    slot = next(slot);
+    stage(s2, std::true_type{}, integral_constant<bool, (SLOTS + 2) % 4 == 0>{}, s + 2, slot);
+    slot = next(slot);
+    stage(s3, std::true_type{}, integral_constant<bool, (SLOTS + 3) % 4 == 0>{}, s + 3, slot);
+    slot = next(slot);
+    read_scales(s + 4);  // they landed with stage s + 4, before the last barrier
     take_scales();
   }
-  load_scales(s + 4);
-  const int turn = s + 3;
-  auto shift_scales = [&]() {
-    sw = s == turn ? sw_next : sw >> 8;
+  auto shift_scales = [&]() {  // to the bytes of stage s + 1
+    read_scales(s + 1);
+    sw = (s & 3) == 3 ? sw_next : sw >> 8;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sx[j] = s == turn ? sx_next[j] : sx[j] >> 8;
+    for (int j = 0; j < FJ; ++j) sx[j] = (s & 3) == 3 ? sx_next[j] : sx[j] >> 8;
   };
-  for (; s + 2 < nk; ++s) {  // at most three
-    stage(s0, std::true_type{}, s);
+  for (; s + SLOTS < nk; ++s) {  // at most three
+    stage(s0, std::true_type{}, std::true_type{}, s, slot);  // (scale words that are there already: the same again)
+    slot = next(slot);
     shift_scales();
   }
   for (; s < nk; ++s) {
-    stage(s0, std::false_type{}, s);
+    stage(s0, std::false_type{}, std::false_type{}, s, slot);
+    slot = next(slot);
     shift_scales();
   }
 
-  // lane: row of y 128 wm + 32 j + r32, outputs 64 wn + 32 i + 8 e + 4 half .. + 3
-  const float* bias = a.bias ? a.bias + (int64_t)t.expert * a.N : nullptr;
-  const bool vec = (a.N & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
+  // A lane holds row r32 of 32 (FJ wm + j), outputs 32 i + 8 e + 4 half .. + 3: turned through LDS (no longer
+  // read by anyone), 32 rows at a time in the wave's own part, so that each row's stores are whole cache lines.
+  // 16-byte piece c of row r is kept at c ^ key(r), as above.
+  landed(s0);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  constexpr int RB = 128 * FI, PIECES = 8 * FI;  // bytes and pieces of a row
+  static_assert(T::WAVES * 32 * RB <= T::LDS, "the waves' parts");
+  auto key = [](int r) { return FI == 1 ? (r >> 1) & 7 : r & 15; };
+  float* turn = reinterpret_cast<float*>(lds + wave * (32 * RB));
+  const float* bias = a.bias && a.S == 1 ? a.bias + (int64_t)t.expert * a.N : nullptr;
+  float* part = a.S > 1 ? a.part + (int64_t)split * a.M * a.N : nullptr;
+  const bool out_f32 = part || !a.y_bf16;
+  float* yf = part ? part : static_cast<float*>(a.y);
+  const int nw = n0 + 32 * FI * wn;  // the wave's first output
+  const bool vec = part ? (a.N & 3) == 0
+                        : ((uintptr_t)a.y & 15) == 0 && (a.N & (out_f32 ? 3 : 7)) == 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int m = 128 * wm + 32 * j + r32;
-    if (m >= t.rows) continue;
-    const int64_t row = (int64_t)(t.row0 + m) * a.N;
+  for (int j = 0; j < FJ; ++j) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < FI; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int n = n0 + 64 * wn + 32 * i + 8 * e + 4 * half;
-        float v[4];
+        const int c = (8 * i + 2 * e + half) ^ key(r32);
+        *reinterpret_cast<f32x4*>(turn + r32 * (RB / 4) + 4 * c) =
+            f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+      }
+    __builtin_amdgcn_wave_barrier();
+    const int m0 = 32 * (FJ * wm + j);
+    if (vec && out_f32) {
+#pragma unroll 2
+      for (int it = 0; it < PIECES / 2; ++it) {
+        const int r = it * (64 / PIECES) + lane / PIECES, c = lane % PIECES, n = nw + 4 * c;
+        f32x4 v = *reinterpret_cast<const f32x4*>(turn + r * (RB / 4) + 4 * (c ^ key(r)));
+        if (m0 + r < t.rows && n < a.N) {
+          if (bias)
 #pragma unroll
-        for (int z = 0; z < 4; ++z) v[z] = acc[i][j][4 * e + z];
-        if (bias)
-#pragma unroll
-          for (int z = 0; z < 4; ++z) v[z] += n + z < a.N ? bias[n + z] : 0.f;
-        if (vec && n + 4 <= a.N) {
-          if (WIDE)
-            *reinterpret_cast<float4*>(static_cast<float*>(a.y) + row + n) = make_float4(v[0], v[1], v[2], v[3]);
-          else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + row + n) =
-                make_uint2(f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
-                           f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16));
-        } else {
-#pragma unroll
-          for (int z = 0; z < 4; ++z)
-            if (n + z < a.N) fp8_store(a, row + n + z, v[z]);
+            for (int z = 0; z < 4; ++z) v[z] += bias[n + z];
+          *reinterpret_cast<f32x4*>(yf + (int64_t)(t.row0 + m0 + r) * a.N + n) = v;
         }
       }
+    } else if (vec) {
+      constexpr int PAIRS = PIECES / 2;
+#pragma unroll 2
+      for (int it = 0; it < PAIRS / 2; ++it) {
+        const int r = it * (64 / PAIRS) + lane / PAIRS, c = 2 * (lane % PAIRS), n = nw + 4 * c;
+        f32x4 v = *reinterpret_cast<const f32x4*>(turn + r * (RB / 4) + 4 * (c ^ key(r)));
+        f32x4 u = *reinterpret_cast<const f32x4*>(turn + r * (RB / 4) + 4 * ((c + 1) ^ key(r)));
+        if (m0 + r < t.rows && n < a.N) {
+          if (bias)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) v[z] += bias[n + z], u[z] += bias[n + 4 + z];
+          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.y) + (int64_t)(t.row0 + m0 + r) * a.N + n) =
+              u32x4{f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16), f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16),
+                    f32_to_bf16_rne(u[0]) | (f32_to_bf16_rne(u[1]) << 16), f32_to_bf16_rne(u[2]) | (f32_to_bf16_rne(u[3]) << 16)};
+        }
+      }
+    } else {
+      for (int it = 0; it < 32 * 32 * FI / 64; ++it) {
+        const int o = it * 64 + lane, r = o / (32 * FI), q = o % (32 * FI), n = nw + q;
+        float v = turn[r * (RB / 4) + 4 * ((q >> 2) ^ key(r)) + (q & 3)];
+        if (m0 + r < t.rows && n < a.N) {
+          if (bias) v += bias[n];
+          const int64_t o64 = (int64_t)(t.row0 + m0 + r) * a.N + n;
+          if (part)
+            part[o64] = v;
+          else
+            fp8_store(a, o64, v);
+        }
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
   }
+}
+
+template <int WM, int WN, int FJ, int FI, int SLOTS>
+void tile_launch(const Fp8Args& a, const Fp8Plan& p, hipStream_t s) {
+  const dim3 grid((unsigned)(p.tiles_n * p.tiles_m * p.S)), block(64 * WM * WN);
+  if (p.wide)
+    hipLaunchKernelGGL((fp8_tile<true, WM, WN, FJ, FI, SLOTS>), grid, block, 0, s, a, (int)p.tiles_n, (int)p.tiles_m);
+  else
+    hipLaunchKernelGGL((fp8_tile<false, WM, WN, FJ, FI, SLOTS>), grid, block, 0, s, a, (int)p.tiles_n, (int)p.tiles_m);
 }
 
 }  // namespace
 
-hipError_t launch_fp8_tile256(const Fp8Args& a, const Fp8Plan& p, hipStream_t s) {
-  const dim3 grid((unsigned)(p.tiles_n * p.tiles_m));
-  if (a.y_bf16)
-    hipLaunchKernelGGL((fp8_tile256<false>), grid, dim3(512), 0, s, a, (int)p.tiles_n, (int)p.tiles_m);
-  else
-    hipLaunchKernelGGL((fp8_tile256<true>), grid, dim3(512), 0, s, a, (int)p.tiles_n, (int)p.tiles_m);
+hipError_t launch_fp8_tile(const Fp8Args& a, const Fp8Plan& p, hipStream_t s) {
+  switch (p.kernel) {
+    case kFp8Tile32: tile_launch<1, 2, 1, 1, 3>(a, p, s); break;
+    case kFp8Tile64: tile_launch<2, 4, 1, 1, 3>(a, p, s); break;
+    case kFp8Tile128: tile_launch<2, 2, 2, 2, 2>(a, p, s); break;
+    default: tile_launch<2, 4, 4, 2, 2>(a, p, s); break;
+  }
   return hipGetLastError();
 }
 

@@ -14,9 +14,9 @@
 // consecutive bytes of each of its 16 rows, and the block's two instructions
 // share their cache lines.
 //
-// Bound: the weight's bytes (each weight row is read once for up to 64 rows of
+// Bound: the weight's bytes (each weight row is read once for up to 16 rows of
 // x).  Operands go from memory straight to registers.  A workgroup owns
-// 16 RW outputs and 16 NT rows of x; its waves share the sum (wave w takes
+// 16 outputs and 16 rows of x; its waves share the sum (wave w takes
 // blocks w, w + waves, ...) so that a layer with few outputs still has enough
 // loads in flight, and add their parts in wave order through LDS.  A sum that
 // is split over workgroups as well leaves its parts in the workspace for
@@ -30,135 +30,111 @@ namespace hxq {
 
 namespace {
 
-template <int RW, int NT, int WAVES>
+template <int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void fp8_skinny(Fp8Args a, int tiles_n, int tiles_m) {
-  constexpr int TN = 16 * RW, TM = 16 * NT;
-  extern __shared__ float red[];  // [WAVES][TM][TN]
+  __shared__ float red[WAVES][16][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   int b = blockIdx.x;
   const int tn = b % tiles_n;
   b /= tiles_n;
   const int tm = b % tiles_m, split = b / tiles_m;
-  const RowTile t = fp8_row_tile(a, tm, TM);
+  const RowTile t = fp8_row_tile(a, tm, 16);
   if (t.rows <= 0) return;  // past the last expert's rows (uniform over the workgroup)
-  const int n0 = tn * TN;
+  const int n0 = tn * 16, n = min(n0 + l16, a.N - 1);
   const int nb = (a.N + 127) >> 7;
   const int kb1 = min((split + 1) * a.kbs, a.Kp >> 7);
-
-  const uint8_t* wp[RW];
-  const uint8_t* wsp[RW];
-#pragma unroll
-  for (int i = 0; i < RW; ++i) {
-    const int n = min(n0 + 16 * i + l16, a.N - 1);
-    wp[i] = a.w + ((int64_t)t.expert * a.N + n) * a.Kp + 16 * g;
-    wsp[i] = a.ws + ((int64_t)t.expert * nb + (n >> 7)) * a.Gs;
-  }
-  const uint8_t* xp[NT];
-  const uint8_t* xsp[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t r = fp8_x_row(a, t.row0 + min(16 * j + l16, t.rows - 1));
-    xp[j] = a.x + r * a.Kp + 16 * g;
-    xsp[j] = a.xs + r * a.Gs;
-  }
-  f32x4 acc[RW][NT];
-#pragma unroll
-  for (int i = 0; i < RW; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
+  const uint8_t* wp = a.w + ((int64_t)t.expert * a.N + n) * a.Kp + 16 * g;
+  const uint8_t* wsp = a.ws + ((int64_t)t.expert * nb + (n >> 7)) * a.Gs;
+  const int64_t r = fp8_x_row(a, t.row0 + min(l16, t.rows - 1));
+  const uint8_t* xp = a.x + r * a.Kp + 16 * g;
+  const uint8_t* xsp = a.xs + r * a.Gs;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
   for (int kb = split * a.kbs + wave; kb < kb1; kb += WAVES) {
     const int64_t k = (int64_t)kb << 7;
-    i32x8 wa[RW], xb[NT];
-    float sa[RW], sb[NT];
+    const i32x4 w0 = *reinterpret_cast<const i32x4*>(wp + k), w1 = *reinterpret_cast<const i32x4*>(wp + k + 64);
+    const i32x4 x0 = *reinterpret_cast<const i32x4*>(xp + k), x1 = *reinterpret_cast<const i32x4*>(xp + k + 64);
+    const float sw = __uint_as_float((uint32_t)wsp[kb] << 23), sx = __uint_as_float((uint32_t)xsp[kb] << 23);
 #pragma unroll
-    for (int i = 0; i < RW; ++i) {
-      const i32x4 lo = *reinterpret_cast<const i32x4*>(wp[i] + k), hi = *reinterpret_cast<const i32x4*>(wp[i] + k + 64);
-      wa[i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      sa[i] = __uint_as_float((uint32_t)wsp[i][kb] << 23);
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const i32x4 lo = *reinterpret_cast<const i32x4*>(xp[j] + k), hi = *reinterpret_cast<const i32x4*>(xp[j] + k + 64);
-      xb[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      sb[j] = __uint_as_float((uint32_t)xsp[j][kb] << 23);
-    }
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {  // 8 bytes of each lane: 32 of the block's k
-      bf16x8 wv[RW], xv[NT];
-#pragma unroll
-      for (int i = 0; i < RW; ++i) wv[i] = widen8(wa[i][2 * p], wa[i][2 * p + 1], sa[i]);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) xv[j] = widen8(xb[j][2 * p], xb[j][2 * p + 1], sb[j]);
-#pragma unroll
-      for (int i = 0; i < RW; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[i], xv[j], acc[i][j], 0, 0, 0);
+    for (int p = 0; p < 2; ++p) {  // 8 bytes of each lane: 32 of the block's k
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w0[2 * p], w0[2 * p + 1], sw),
+                                                   widen8(x0[2 * p], x0[2 * p + 1], sx), acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w1[2 * p], w1[2 * p + 1], sw),
+                                                   widen8(x1[2 * p], x1[2 * p + 1], sx), acc, 0, 0, 0);
     }
   }
 
-  // lane (token l16, g) holds outputs 4 g .. + 3 of each 16 x 16 tile
-#pragma unroll
-  for (int i = 0; i < RW; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      *reinterpret_cast<f32x4*>(red + ((wave * TM + 16 * j + l16) * TN + 16 * i + 4 * g)) = acc[i][j];
+  // lane (token l16, g) holds outputs 4 g .. + 3
+  *reinterpret_cast<f32x4*>(&red[wave][l16][4 * g]) = acc;
   __syncthreads();
-  for (int o = threadIdx.x; o < TM * TN; o += 64 * WAVES) {
-    const int m = o / TN, n = n0 + o % TN;
-    if (m >= t.rows || n >= a.N) continue;
-    float v = red[o];
-    for (int w = 1; w < WAVES; ++w) v += red[w * TM * TN + o];
-    const int64_t at = (int64_t)(t.row0 + m) * a.N + n;
-    if (a.S > 1) {
-      a.part[(int64_t)split * a.M * a.N + at] = v;
-    } else {
-      if (a.bias) v += a.bias[(int64_t)t.expert * a.N + n];
-      fp8_store(a, at, v);
-    }
+  if (threadIdx.x >= 256) return;
+  const int m = threadIdx.x >> 4, c = threadIdx.x & 15;
+  if (m >= t.rows || n0 + c >= a.N) return;
+  float v = red[0][m][c];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) v += red[w][m][c];
+  const int64_t at = (int64_t)(t.row0 + m) * a.N + n0 + c;
+  if (a.S > 1) {
+    a.part[(int64_t)split * a.M * a.N + at] = v;
+  } else {
+    if (a.bias) v += a.bias[(int64_t)t.expert * a.N + n0 + c];
+    fp8_store(a, at, v);
   }
 }
 
-// y = bias + the splits' parts, in order.  Rows past the last expert's are
-// left as they are.
+// y = bias + the splits' parts, in order: V consecutive outputs of a row to a
+// thread, four splits' loads in flight.  Rows past the last expert's are left
+// as they are.
+template <int V>
 __global__ __launch_bounds__(256) void fp8_sum(Fp8Args a) {
+  typedef float vec __attribute__((ext_vector_type(V)));
   const int64_t total = (int64_t)fp8_rows_end(a) * a.N, stride = (int64_t)a.M * a.N;
-  for (int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x; o < total; o += (int64_t)gridDim.x * 256) {
-    float v = 0.f;
-    for (int s = 0; s < a.S; ++s) v += a.part[s * stride + o];
+  for (int64_t o = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; o < total; o += (int64_t)gridDim.x * (256 * V)) {
+    vec v = 0.f;
+    const float* p = a.part + o;
+    int s = 0;
+    for (; s + 4 <= a.S; s += 4, p += 4 * stride) {
+      vec u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const vec*>(p + i * stride);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v += u[i];
+    }
+    for (; s < a.S; ++s, p += stride) v += *reinterpret_cast<const vec*>(p);
     if (a.bias) {
       const int m = (int)(o / a.N);
       const int e = a.offsets ? fp8_expert_of(a, m) : 0;
-      v += a.bias[(int64_t)e * a.N + (o - (int64_t)m * a.N)];
+      const float* b = a.bias + (int64_t)e * a.N + (o - (int64_t)m * a.N);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] += b[i];
     }
-    fp8_store(a, o, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) fp8_store(a, o + i, v[i]);
   }
 }
 
-template <int RW, int NT, int WAVES>
+template <int WAVES>
 void skinny_launch(const Fp8Args& a, const Fp8Plan& p, hipStream_t s) {
-  const int lds = WAVES * RW * NT * 256 * 4;
-  hipLaunchKernelGGL((fp8_skinny<RW, NT, WAVES>), dim3((unsigned)(p.tiles_n * p.tiles_m * p.S)), dim3(64 * WAVES), lds,
-                     s, a, (int)p.tiles_n, (int)p.tiles_m);
+  hipLaunchKernelGGL(fp8_skinny<WAVES>, dim3((unsigned)(p.tiles_n * p.tiles_m * p.S)), dim3(64 * WAVES), 0, s, a,
+                     (int)p.tiles_n, (int)p.tiles_m);
 }
 
 }  // namespace
 
 hipError_t launch_fp8_skinny(const Fp8Args& a, const Fp8Plan& p, hipStream_t s) {
-  if (p.kernel == kFp8Skinny16)
-    p.waves == 4 ? skinny_launch<1, 1, 4>(a, p, s) : skinny_launch<1, 1, 8>(a, p, s);
-  else if (p.kernel == kFp8Skinny32)
-    skinny_launch<2, 2, 4>(a, p, s);
-  else
-    skinny_launch<4, 4, 4>(a, p, s);
+  p.waves == 4 ? skinny_launch<4>(a, p, s) : skinny_launch<8>(a, p, s);
   return hipGetLastError();
 }
 
 hipError_t launch_fp8_sum(const Fp8Args& a, hipStream_t s) {
-  const int64_t wgs = ((int64_t)a.M * a.N + 1023) / 1024;
-  hipLaunchKernelGGL(fp8_sum, dim3((unsigned)(wgs < 4096 ? wgs : 4096)), dim3(256), 0, s, a);
+  const bool vec = a.N % 4 == 0;  // (the workspace's parts are 256-byte aligned)
+  const int64_t n = (int64_t)a.M * a.N / (vec ? 4 : 1), wgs = (n + 255) / 256;
+  const dim3 grid((unsigned)(wgs < 8192 ? wgs : 8192));
+  if (vec)
+    hipLaunchKernelGGL(fp8_sum<4>, grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL(fp8_sum<1>, grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
