@@ -58,11 +58,11 @@ BAD = [
     (linear, dict(x=FAKE + 1), ALIGN), (linear, dict(x=FAKE + 2, x_dtype=0), ALIGN), (linear, dict(x=FAKE + 8, x_dtype=2, xs=FAKE), ALIGN),
     (linear, dict(x_dtype=2, xs=FAKE + 1), ALIGN), (linear, dict(wq=FAKE + 8), ALIGN), (linear, dict(ws=FAKE + 2), ALIGN),
     (linear, dict(bias=FAKE + 2), ALIGN), (linear, dict(y=FAKE + 2), ALIGN), (linear, dict(y=FAKE + 1, y_dtype=1), ALIGN),
-    (linear, dict(work=FAKE + 8), ALIGN), (linear, dict(work=None, nbytes=0), UNSUP), (linear, dict(nbytes=1), UNSUP),
+    (linear, dict(work=FAKE + 8), ALIGN), (linear, dict(M=100, work=None, nbytes=0), UNSUP), (linear, dict(M=100, nbytes=1), UNSUP),
     (experts, dict(E=0), SHAPE), (experts, dict(E=65536), SHAPE), (experts, dict(offsets=None), NULL),
     (experts, dict(Mx=3), SHAPE), (experts, dict(Mx=0, rows=FAKE), SHAPE), (experts, dict(Mx=-1, rows=FAKE), SHAPE),
     (experts, dict(rows=FAKE + 2), ALIGN), (experts, dict(offsets=FAKE + 2), ALIGN), (experts, dict(x=None), NULL),
-    (experts, dict(nbytes=1), UNSUP), (experts, dict(x_dtype=7), DTYPE),
+    (experts, dict(M=100, Mx=100, nbytes=1), UNSUP), (experts, dict(x_dtype=7), DTYPE),
     (norm, dict(x_dtype=2), DTYPE), (norm, dict(out_dtype=3), DTYPE), (norm, dict(res=FAKE, res_dtype=2, res_out=FAKE), DTYPE),
     (norm, dict(M=-1), SHAPE), (norm, dict(K=HUGE), SHAPE), (norm, dict(eps=-1.0), UNSUP), (norm, dict(eps=float("nan")), UNSUP),
     (norm, dict(x=None), NULL), (norm, dict(out=None), NULL), (norm, dict(res=FAKE), NULL), (norm, dict(res_out=FAKE), NULL),
@@ -104,7 +104,8 @@ def test_workspace_queries(L):
             for K in (1, 128, 2048, 11008, 70000):
                 rows = M * (-(-K // 128) * 128)
                 with_x, without = q(1, M, N, K), q(2, M, N, K)
-                assert q(0, M, N, K) == with_x >= rows + without
+                # room for the converted rows, unless there are few enough for every workgroup to convert them
+                assert q(0, M, N, K) == with_x and (with_x >= rows + without or M * K <= 8 * 11008)
                 part = without // (4 * M * N)
                 assert without == part * 4 * M * N and part != 1  # whole partial matrices, two or more
     e = L.hxq_linear_fwd_fp8_experts_workspace

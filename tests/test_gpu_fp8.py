@@ -358,7 +358,7 @@ def test_norm_in_place_and_special_rows():
 
 
 @pytest.mark.parametrize("dres,dw", [(False, True), (True, True), (True, False)])
-@pytest.mark.parametrize("M,K", [(1, 1), (3, 7), (5, 512), (2100, 513), (4500, 130), (700, 2048), (3, 2056), (1500, 4096), (6, 11008), (5, 20001)])
+@pytest.mark.parametrize("M,K", [(1, 1), (3, 7), (5, 512), (2100, 513), (4500, 130), (700, 2048), (3, 2056), (1500, 4096), (6, 11008), (5, 20001), (520, 12801)])
 def test_norm_gradient(M, K, dres, dw):
     h = make(M + K, M, K, dtype=BF16 if K % 2 else F32)
     dy = make(M + K + 1, M, K, dtype=BF16 if M % 2 else F32)

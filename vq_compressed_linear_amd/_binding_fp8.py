@@ -21,6 +21,7 @@ E8M0 = torch.float8_e8m0fnu
 
 _DTYPE = {torch.float32: B.HXQ_F32, torch.bfloat16: B.HXQ_BF16, E4M3: B.HXQ_E4M3}
 _NO_GUARD = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def fp8_columns(k: int) -> int:
@@ -41,9 +42,9 @@ def _dtype(t, what: str, e4m3: bool = False) -> int:
 
 
 def _tensor(t, what: str, dtype, shape) -> None:
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s %s tensor, got %s %s" % (what, dtype, tuple(shape), t.dtype,
-                                                                              tuple(t.shape)))
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s %s tensor, got %s %s%s" % (
+            what, dtype, tuple(shape), t.dtype, tuple(t.shape), "" if t.is_contiguous() else ", not contiguous"))
 
 
 def _matrix(t, what: str):
@@ -52,12 +53,34 @@ def _matrix(t, what: str):
     return t.shape
 
 
-def _on(dev):
+def _device(*tensors) -> int:
+    """Index of the one GPU that every tensor given (None skipped) lives on: the kernels read raw device pointers,
+    and a host tensor's would fault them."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError("every tensor must be on a GPU; got one on %s" % t.device)
+                if dev is not None:
+                    raise ValueError("tensors on different devices: cuda:%d and cuda:%d" % (dev, d))
+                dev = d
+    return dev
+
+
+def _on(dev: int):
     """Launches go to the tensors' device, whichever is current."""
-    return _NO_GUARD if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return _NO_GUARD if torch.cuda.current_device() == dev else torch.cuda.device(dev)
 
 
-def _workspace(workspace, need: int, what: str, dev, stream):
+def _stream(stream, dev: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return B._stream(stream, dev)
+
+
+def _workspace(workspace, need: int, what: str, dev: int, stream):
     """(pointer, bytes) of the caller's workspace, or of one from torch's caching allocator; the tensor is the
     third, to be kept until the launch is queued.  The allocation belongs to the stream of the launch, so its
     memory is not handed out again to work that does not wait for it."""
@@ -85,9 +108,9 @@ def hxq_quant_fp8(x, q, scales, stream=None) -> None:
     dt = _dtype(x, "x")
     _tensor(q, "q", E4M3, (M, fp8_columns(K)))
     _tensor(scales, "scales", E8M0, (M, fp8_scale_columns(K)))
-    dev = B._check_device(x, q, scales)
+    dev = _device(x, q, scales)
     with _on(dev):
-        st = B.lib().hxq_quant_fp8(x.data_ptr(), dt, q.data_ptr(), scales.data_ptr(), M, K, B._stream(stream, dev))
+        st = B.lib().hxq_quant_fp8(x.data_ptr(), dt, q.data_ptr(), scales.data_ptr(), M, K, _stream(stream, dev))
     if st != B.HXQ_OK:
         raise B.HxqError(st, "hxq_quant_fp8")
 
@@ -107,10 +130,10 @@ def hxq_quant_fp8_weight(w, q, scales, qt=None, scales_t=None, stream=None) -> N
     if qt is not None:
         _tensor(qt, "qt", E4M3, lead + (K, fp8_columns(N)))
         _tensor(scales_t, "scales_t", E8M0, lead + ((K + 127) // 128, fp8_scale_columns(N)))
-    dev = B._check_device(w, q, scales, qt, scales_t)
+    dev = _device(w, q, scales, qt, scales_t)
     with _on(dev):
         st = B.lib().hxq_quant_fp8_weight(w.data_ptr(), dt, q.data_ptr(), scales.data_ptr(), B._ptr(qt),
-                                          B._ptr(scales_t), lead[0] if lead else 1, N, K, B._stream(stream, dev))
+                                          B._ptr(scales_t), lead[0] if lead else 1, N, K, _stream(stream, dev))
     if st != B.HXQ_OK:
         raise B.HxqError(st, "hxq_quant_fp8_weight")
 
@@ -147,13 +170,13 @@ def hxq_linear_fwd_fp8(x, x_scales, wq, w_scales, bias, y, stream=None, workspac
     _tensor(y, "y", y.dtype, (M, N))
     if bias is not None:
         _tensor(bias, "bias", torch.float32, (N,))
-    dev = B._check_device(x, x_scales, wq, w_scales, bias, y, workspace)
+    dev = _device(x, x_scales, wq, w_scales, bias, y, workspace)
     lib = B.lib()
     with _on(dev):
         ptr, size, keep = _workspace(workspace, lib.hxq_linear_fwd_fp8_workspace(dt, M, N, K),
                                      "hxq_linear_fwd_fp8_workspace", dev, stream)
         st = lib.hxq_linear_fwd_fp8(x.data_ptr(), dt, B._ptr(x_scales), wq.data_ptr(), w_scales.data_ptr(),
-                                    B._ptr(bias), y.data_ptr(), ydt, M, N, K, ptr, size, B._stream(stream, dev))
+                                    B._ptr(bias), y.data_ptr(), ydt, M, N, K, ptr, size, _stream(stream, dev))
     if st != B.HXQ_OK:
         raise B.HxqError(st, "hxq_linear_fwd_fp8")
 
@@ -179,14 +202,14 @@ def hxq_linear_fwd_fp8_experts(x, x_scales, rows, offsets, wq, w_scales, bias, y
         raise ValueError("x has %d rows, y %d: without `rows` they are the same" % (Mx, M))
     if bias is not None:
         _tensor(bias, "bias", torch.float32, (E, N))
-    dev = B._check_device(x, x_scales, rows, offsets, wq, w_scales, bias, y, workspace)
+    dev = _device(x, x_scales, rows, offsets, wq, w_scales, bias, y, workspace)
     lib = B.lib()
     with _on(dev):
         ptr, size, keep = _workspace(workspace, lib.hxq_linear_fwd_fp8_experts_workspace(dt, Mx, M, E, N, K),
                                      "hxq_linear_fwd_fp8_experts_workspace", dev, stream)
         st = lib.hxq_linear_fwd_fp8_experts(x.data_ptr(), dt, B._ptr(x_scales), B._ptr(rows), offsets.data_ptr(),
                                             wq.data_ptr(), w_scales.data_ptr(), B._ptr(bias), y.data_ptr(), ydt, Mx,
-                                            M, E, N, K, ptr, size, B._stream(stream, dev))
+                                            M, E, N, K, ptr, size, _stream(stream, dev))
     if st != B.HXQ_OK:
         raise B.HxqError(st, "hxq_linear_fwd_fp8_experts")
 
@@ -220,10 +243,10 @@ def hxq_rms_norm(x, weight, eps: float, out, scales=None, residual=None, residua
         _tensor(residual_out, "residual_out", residual.dtype, (M, K))
     if rstd is not None:
         _tensor(rstd, "rstd", torch.float32, (M,))
-    dev = B._check_device(x, weight, out, scales, residual, residual_out, rstd)
+    dev = _device(x, weight, out, scales, residual, residual_out, rstd)
     with _on(dev):
         st = B.lib().hxq_rms_norm(x.data_ptr(), dt, B._ptr(residual), rdt, B._ptr(weight), eps, B._ptr(residual_out),
-                                  out.data_ptr(), odt, B._ptr(scales), B._ptr(rstd), M, K, B._stream(stream, dev))
+                                  out.data_ptr(), odt, B._ptr(scales), B._ptr(rstd), M, K, _stream(stream, dev))
     if st != B.HXQ_OK:
         raise B.HxqError(st, "hxq_rms_norm")
 
@@ -243,13 +266,13 @@ def hxq_rms_norm_bwd(dy, h, weight, rstd, dx, dweight=None, dresidual=None, stre
         _tensor(dweight, "dweight", torch.float32, (K,))
     if dresidual is not None:
         _tensor(dresidual, "dresidual", torch.float32, (M, K))
-    dev = B._check_device(dy, h, weight, rstd, dx, dweight, dresidual, workspace)
+    dev = _device(dy, h, weight, rstd, dx, dweight, dresidual, workspace)
     lib = B.lib()
     with _on(dev):
         need = 0 if dweight is None else lib.hxq_rms_norm_bwd_workspace(M, K)
         ptr, size, keep = _workspace(workspace, need, "hxq_rms_norm_bwd_workspace", dev, stream)
         st = lib.hxq_rms_norm_bwd(dy.data_ptr(), dt, h.data_ptr(), hdt, B._ptr(weight), rstd.data_ptr(),
                                   B._ptr(dresidual), dx.data_ptr(), B._ptr(dweight), M, K, ptr, size,
-                                  B._stream(stream, dev))
+                                  _stream(stream, dev))
     if st != B.HXQ_OK:
         raise B.HxqError(st, "hxq_rms_norm_bwd")

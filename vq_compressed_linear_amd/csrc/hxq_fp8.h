@@ -42,12 +42,12 @@ struct NormBwdArgs {
   const float* dsum;      // [M][K] or nullptr
   float* dx;              // [M][K]
   float* dweight;         // [K] or nullptr
-  float* part;            // [norm_bwd_teams()][K] when dweight
+  float* part;            // [norm_bwd_parts()][K] when dweight
   int64_t M;
   int K;
   int dy_dtype, h_dtype;
 };
-int64_t norm_bwd_teams(int64_t M, int64_t K);  // partial rows of the weight's gradient
+int64_t norm_bwd_parts(int64_t M, int64_t K);  // partial rows of the weight's gradient
 hipError_t launch_rms_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
 
 hipError_t launch_quant_rows(const void* x, int x_dtype, uint8_t* q, uint8_t* scales, int64_t M, int K,
@@ -60,6 +60,8 @@ hipError_t launch_quant_weight(const void* w, int w_dtype, uint8_t* q, uint8_t* 
 struct Fp8Args {
   const uint8_t* x;        // [Mx][Kp] e4m3
   const uint8_t* xs;       // [Mx][Gs]
+  const void* xf;          // [Mx][K] float32 or bf16, where the kernel converts x itself
+  int x_dtype;             // its type then, else HXQ_E4M3
   const int32_t* rows;     // [M] row of x for each row of y, or nullptr (the row itself); experts only
   const int32_t* offsets;  // [E + 1] first row of each expert, or nullptr (one layer)
   const uint8_t* w;        // [E][N][Kp] e4m3
@@ -69,7 +71,7 @@ struct Fp8Args {
   int y_bf16;
   float* part;             // [S][M][N] partial sums when S > 1
   int64_t Mx;
-  int M, N, Kp, Gs, E;
+  int M, N, K, Kp, Gs, E;
   int S, kbs;              // splits of the sum, 128-blocks in each
 };
 
@@ -77,6 +79,7 @@ struct Fp8Args {
 struct Fp8Plan {
   int kernel;       // one of Fp8Kernel
   bool wide;        // operands widened to bf16 (tile kernels)
+  bool converts;    // the kernel converts a float32 or bf16 x itself
   int waves;        // waves that share a tile's sum (skinny kernels)
   int S, kbs;
   int64_t tiles_m, tiles_n;

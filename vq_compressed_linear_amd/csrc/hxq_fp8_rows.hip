@@ -177,16 +177,17 @@ void norm_launch_res(const NormArgs& a, hipStream_t s) {
 
 // Teams of TPR threads walk the rows team, team + teams, ...; a thread keeps
 // its columns' part of the weight's gradient in registers over its team's rows
-// (NCH > 0) or in its team's partial row in memory (NCH == 0), and the second
-// launch adds the partial rows in order.
+// (NCH > 0; the four waves of a workgroup then add theirs in LDS) or in its
+// workgroup's partial row in memory (NCH == 0), and the second launch adds the
+// workgroups' partial rows in order.
 template <int TPR, int NCH, int DT, int HT>
-__global__ __launch_bounds__(256) void rms_norm_bwd_rows(NormBwdArgs a, int64_t teams) {
+__global__ __launch_bounds__(256) void rms_norm_bwd_rows(NormBwdArgs a) {
   __shared__ float slot[2][4];
+  __shared__ float wave_dw[TPR == 64 ? 4 : 1][TPR == 64 ? 512 * NCH : 1];
   const int t = threadIdx.x % TPR;
-  const int64_t team = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
-  if (TPR == 64 && team >= teams) return;  // a whole wave
+  const int64_t team = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR, teams = (int64_t)gridDim.x * (256 / TPR);
   const int K = a.K;
-  float* part = a.part ? a.part + team * (int64_t)K : nullptr;
+  float* part = a.part ? a.part + blockIdx.x * (int64_t)K : nullptr;
   if constexpr (NCH > 0) {
     float w[NCH][8], dw[NCH][8];
 #pragma unroll
@@ -239,7 +240,16 @@ __global__ __launch_bounds__(256) void rms_norm_bwd_rows(NormBwdArgs a, int64_t 
         }
       }
     }
-    if (part) {
+    if (!part) return;
+    if constexpr (TPR == 64) {
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wave_dw[threadIdx.x >> 6][(c * 64 + t) * 8 + i] = dw[c][i];
+      __syncthreads();
+      for (int col = threadIdx.x; col < K; col += 256)
+        part[col] = (wave_dw[0][col] + wave_dw[1][col]) + (wave_dw[2][col] + wave_dw[3][col]);
+    } else {
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         const int col = (c * TPR + t) * 8;
@@ -286,41 +296,56 @@ __global__ __launch_bounds__(256) void rms_norm_bwd_rows(NormBwdArgs a, int64_t 
   }
 }
 
-// dw[k] = sum of the teams' partial rows: 16 columns x 16 runs of teams to a
-// workgroup, each run summed in order, then the runs in order.
-__global__ __launch_bounds__(256) void norm_dw_sum(const float* part, float* dw, int64_t teams, int K) {
-  __shared__ float s[16][17];
-  const int c = threadIdx.x & 15, run = threadIdx.x >> 4;
-  const int col = blockIdx.x * 16 + c;
-  float v = 0.f;
-  if (col < K)
-    for (int64_t p = run; p < teams; p += 16) v += part[p * (int64_t)K + col];
-  s[run][c] = v;
-  __syncthreads();
-  if (run == 0 && col < K) {
-    float o = 0.f;
+// dw[k] = sum of the partial rows: 64 columns x 64 runs of rows to a
+// workgroup (16 lanes of 4 columns: 256-byte pieces), each run summed in
+// order, then the runs in order.
+__global__ __launch_bounds__(1024) void norm_dw_sum(const float* part, float* dw, int64_t rows, int K) {
+  __shared__ float s[64][64];
+  const int c = 4 * (threadIdx.x & 15), run = threadIdx.x >> 4;
+  const int col = blockIdx.x * 64 + c;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (col + 4 <= K) {
+    struct __attribute__((packed, aligned(4))) P {
+      float f[4];
+    };
+#pragma unroll 4
+    for (int64_t p = run; p < rows; p += 64) {
+      const P u = *reinterpret_cast<const P*>(part + p * (int64_t)K + col);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o += s[i][c];
-    dw[col] = o;
+      for (int i = 0; i < 4; ++i) v[i] += u.f[i];
+    }
+  } else {
+    for (int64_t p = run; p < rows; p += 64)
+      for (int i = 0; i < 4; ++i)
+        if (col + i < K) v[i] += part[p * (int64_t)K + col + i];
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[run][c + i] = v[i];
+  __syncthreads();
+  const int o = blockIdx.x * 64 + threadIdx.x;
+  if (threadIdx.x >= 64 || o >= K) return;
+  float sum = 0.f;
+#pragma unroll 16
+  for (int i = 0; i < 64; ++i) sum += s[i][threadIdx.x];
+  dw[o] = sum;
 }
 
 bool bwd_waves(int64_t K) { return K <= 2048; }  // a wave to a row, else a workgroup
 
 template <int DT, int HT>
-void norm_bwd_launch(const NormBwdArgs& a, int64_t teams, hipStream_t s) {
+void norm_bwd_launch(const NormBwdArgs& a, hipStream_t s) {
   const int K = a.K;
-  const unsigned g1 = (unsigned)teams, g4 = (unsigned)((teams + 3) / 4);
+  const dim3 grid((unsigned)norm_bwd_parts(a.M, K));
   if (K <= 512)
-    hipLaunchKernelGGL((rms_norm_bwd_rows<64, 1, DT, HT>), dim3(g4), dim3(256), 0, s, a, teams);
+    hipLaunchKernelGGL((rms_norm_bwd_rows<64, 1, DT, HT>), grid, dim3(256), 0, s, a);
   else if (bwd_waves(K))
-    hipLaunchKernelGGL((rms_norm_bwd_rows<64, 4, DT, HT>), dim3(g4), dim3(256), 0, s, a, teams);
+    hipLaunchKernelGGL((rms_norm_bwd_rows<64, 4, DT, HT>), grid, dim3(256), 0, s, a);
   else if (K <= 4096)
-    hipLaunchKernelGGL((rms_norm_bwd_rows<256, 2, DT, HT>), dim3(g1), dim3(256), 0, s, a, teams);
+    hipLaunchKernelGGL((rms_norm_bwd_rows<256, 2, DT, HT>), grid, dim3(256), 0, s, a);
   else if (K <= 12288)
-    hipLaunchKernelGGL((rms_norm_bwd_rows<256, 6, DT, HT>), dim3(g1), dim3(256), 0, s, a, teams);
+    hipLaunchKernelGGL((rms_norm_bwd_rows<256, 6, DT, HT>), grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((rms_norm_bwd_rows<256, 0, DT, HT>), dim3(g1), dim3(256), 0, s, a, teams);
+    hipLaunchKernelGGL((rms_norm_bwd_rows<256, 0, DT, HT>), grid, dim3(256), 0, s, a);
 }
 
 // ------------------------------------------------------------ conversion
@@ -433,28 +458,29 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Teams of the gradient: enough to fill the GPU (8 workgroups to a CU would be
-// 2048), few enough that the partial rows of dw stay a small part of the bytes.
-int64_t norm_bwd_teams(int64_t M, int64_t K) {
-  const int64_t most = bwd_waves(K) ? 2048 : 512;
-  return M < most ? M : most;
+// Workgroups of the gradient, each with a partial row of dw: two to a CU, few
+// enough that the partial rows stay a small part of the bytes.
+int64_t norm_bwd_parts(int64_t M, int64_t K) {
+  const int64_t need = bwd_waves(K) ? (M + 3) / 4 : M;
+  return need < 512 ? need : 512;
 }
 
 hipError_t launch_rms_norm_bwd(const NormBwdArgs& a, hipStream_t s) {
-  const int64_t teams = norm_bwd_teams(a.M, a.K);
-  if (teams == 0) {
-    // no rows: only the (zero) sum below
-  } else if (a.dy_dtype == kF32 && a.h_dtype == kF32)
-    norm_bwd_launch<kF32, kF32>(a, teams, s);
-  else if (a.dy_dtype == kF32)
-    norm_bwd_launch<kF32, kBf16>(a, teams, s);
-  else if (a.h_dtype == kF32)
-    norm_bwd_launch<kBf16, kF32>(a, teams, s);
-  else
-    norm_bwd_launch<kBf16, kBf16>(a, teams, s);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.dweight) return e;
-  hipLaunchKernelGGL(norm_dw_sum, dim3((unsigned)((a.K + 15) / 16)), dim3(256), 0, s, a.part, a.dweight, teams, a.K);
+  if (a.M > 0) {
+    if (a.dy_dtype == kF32 && a.h_dtype == kF32)
+      norm_bwd_launch<kF32, kF32>(a, s);
+    else if (a.dy_dtype == kF32)
+      norm_bwd_launch<kF32, kBf16>(a, s);
+    else if (a.h_dtype == kF32)
+      norm_bwd_launch<kBf16, kF32>(a, s);
+    else
+      norm_bwd_launch<kBf16, kBf16>(a, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (!a.dweight) return hipSuccess;
+  hipLaunchKernelGGL(norm_dw_sum, dim3((unsigned)((a.K + 63) / 64)), dim3(1024), 0, s, a.part, a.dweight,
+                     norm_bwd_parts(a.M, a.K), a.K);
   return hipGetLastError();
 }
 

@@ -30,9 +30,15 @@ namespace hxq {
 
 namespace {
 
-template <int WAVES>
+// XT: -1 (x is e4m3), or the type of the values that the workgroup converts
+// for itself (hxq_quant_fp8's arithmetic), into LDS: [16 rows][the split's
+// bytes], then the scales.  That saves a launch where x is small (measured:
+// one token through 22016 x 2048 and 2048 x 2048).
+template <int WAVES, int XT>
 __global__ __launch_bounds__(64 * WAVES) void fp8_skinny(Fp8Args a, int tiles_n, int tiles_m) {
+  constexpr int DEPTH = 4;  // blocks of a wave in flight
   __shared__ float red[WAVES][16][16];
+  extern __shared__ __align__(16) uint8_t xlds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   int b = blockIdx.x;
@@ -43,26 +49,69 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_skinny(Fp8Args a, int tiles_n,
   if (t.rows <= 0) return;  // past the last expert's rows (uniform over the workgroup)
   const int n0 = tn * 16, n = min(n0 + l16, a.N - 1);
   const int nb = (a.N + 127) >> 7;
-  const int kb1 = min((split + 1) * a.kbs, a.Kp >> 7);
+  const int kb0 = split * a.kbs, kb1 = min(kb0 + a.kbs, a.Kp >> 7), nk = kb1 - kb0;
   const uint8_t* wp = a.w + ((int64_t)t.expert * a.N + n) * a.Kp + 16 * g;
   const uint8_t* wsp = a.ws + ((int64_t)t.expert * nb + (n >> 7)) * a.Gs;
-  const int64_t r = fp8_x_row(a, t.row0 + min(l16, t.rows - 1));
-  const uint8_t* xp = a.x + r * a.Kp + 16 * g;
-  const uint8_t* xsp = a.xs + r * a.Gs;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-  for (int kb = split * a.kbs + wave; kb < kb1; kb += WAVES) {
-    const int64_t k = (int64_t)kb << 7;
-    const i32x4 w0 = *reinterpret_cast<const i32x4*>(wp + k), w1 = *reinterpret_cast<const i32x4*>(wp + k + 64);
-    const i32x4 x0 = *reinterpret_cast<const i32x4*>(xp + k), x1 = *reinterpret_cast<const i32x4*>(xp + k + 64);
-    const float sw = __uint_as_float((uint32_t)wsp[kb] << 23), sx = __uint_as_float((uint32_t)xsp[kb] << 23);
+  const int row = min(l16, t.rows - 1);
+  const uint8_t *xp, *xsp;  // of block kb0
+  if constexpr (XT < 0) {
+    const int64_t r = fp8_x_row(a, t.row0 + row);
+    xp = a.x + r * a.Kp + 16 * g + ((int64_t)kb0 << 7);
+    xsp = a.xs + r * a.Gs + kb0;
+  }
+  i32x4 w0[DEPTH], w1[DEPTH];
+  float sw[DEPTH];
+  auto load_w = [&](int kb, int d) {  // (past the end the last block again: read, not used)
+    const int k = min(kb + d * WAVES, kb1 - 1);
+    w0[d] = *reinterpret_cast<const i32x4*>(wp + ((int64_t)k << 7));
+    w1[d] = *reinterpret_cast<const i32x4*>(wp + ((int64_t)k << 7) + 64);
+    sw[d] = __uint_as_float((uint32_t)wsp[k] << 23);
+  };
+  if (nk > 0)
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {  // 8 bytes of each lane: 32 of the block's k
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w0[2 * p], w0[2 * p + 1], sw),
-                                                   widen8(x0[2 * p], x0[2 * p + 1], sx), acc, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w1[2 * p], w1[2 * p + 1], sw),
-                                                   widen8(x1[2 * p], x1[2 * p + 1], sx), acc, 0, 0, 0);
+    for (int d = 0; d < DEPTH; ++d) load_w(kb0 + wave, d);
+  if constexpr (XT >= 0) {
+    uint8_t* scales = xlds + t.rows * (nk << 7);
+    for (int q = threadIdx.x >> 4; q < t.rows * nk; q += 4 * WAVES) {  // 16 lanes to a group
+      const int m = q / nk, kb = q - m * nk, col = ((kb0 + kb) << 7) + 8 * (threadIdx.x & 15);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      if (col < a.K) load_row8<XT>(a.xf, fp8_x_row(a, t.row0 + m) * a.K, col, a.K, v);
+      int byte;
+      const uint2 o = quant_group(v, byte);
+      *reinterpret_cast<uint2*>(xlds + (m * nk + kb) * 128 + 8 * (threadIdx.x & 15)) = o;
+      if ((threadIdx.x & 15) == 0) scales[m * nk + kb] = (uint8_t)byte;
     }
+    __syncthreads();
+    xp = xlds + row * (nk << 7) + 16 * g;
+    xsp = scales + row * nk;
+  }
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int kb = kb0 + wave; kb < kb1; kb += DEPTH * WAVES) {
+    i32x4 x0[DEPTH], x1[DEPTH];
+    float sx[DEPTH];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      const int k = min(kb + d * WAVES, kb1 - 1) - kb0;
+      x0[d] = *reinterpret_cast<const i32x4*>(xp + (k << 7));
+      x1[d] = *reinterpret_cast<const i32x4*>(xp + (k << 7) + 64);
+      sx[d] = __uint_as_float((uint32_t)xsp[k] << 23);
+    }
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      if (kb + d * WAVES >= kb1) break;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {  // 8 bytes of each lane: 32 of the block's k
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w0[d][2 * p], w0[d][2 * p + 1], sw[d]),
+                                                     widen8(x0[d][2 * p], x0[d][2 * p + 1], sx[d]), acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w1[d][2 * p], w1[d][2 * p + 1], sw[d]),
+                                                     widen8(x1[d][2 * p], x1[d][2 * p + 1], sx[d]), acc, 0, 0, 0);
+      }
+    }
+    if (kb + DEPTH * WAVES < kb1)
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) load_w(kb + DEPTH * WAVES, d);
   }
 
   // lane (token l16, g) holds outputs 4 g .. + 3
@@ -116,8 +165,14 @@ __global__ __launch_bounds__(256) void fp8_sum(Fp8Args a) {
 
 template <int WAVES>
 void skinny_launch(const Fp8Args& a, const Fp8Plan& p, hipStream_t s) {
-  hipLaunchKernelGGL(fp8_skinny<WAVES>, dim3((unsigned)(p.tiles_n * p.tiles_m * p.S)), dim3(64 * WAVES), 0, s, a,
-                     (int)p.tiles_n, (int)p.tiles_m);
+  const dim3 grid((unsigned)(p.tiles_n * p.tiles_m * p.S)), block(64 * WAVES);
+  const int lds = (a.M < 16 ? a.M : 16) * a.kbs * 129 + 15;
+  if (a.x_dtype == kF32)
+    hipLaunchKernelGGL((fp8_skinny<WAVES, kF32>), grid, block, lds, s, a, (int)p.tiles_n, (int)p.tiles_m);
+  else if (a.x_dtype == kBf16)
+    hipLaunchKernelGGL((fp8_skinny<WAVES, kBf16>), grid, block, lds, s, a, (int)p.tiles_n, (int)p.tiles_m);
+  else
+    hipLaunchKernelGGL((fp8_skinny<WAVES, -1>), grid, block, 0, s, a, (int)p.tiles_n, (int)p.tiles_m);
 }
 
 }  // namespace
