@@ -133,14 +133,16 @@ __global__ __launch_bounds__(64 * WM * WN, FI * FJ > 8 ? 1 : 2) void fp8_tile(Fp
     }
   }
   const uint32_t words0 = lds0 + SLOTS * STAGE;
-  auto request = [&](auto words, int s, uint32_t slot) {
-    if constexpr (decltype(words)::value)
+  auto request_scales = [&](int s) {
 #pragma unroll
-      for (int j = 0; j < T::WPER; ++j)
-        request_words(word_base[j] + (s & ~3), word_off[j], word_to[j] + ((s >> 2) & 1) * T::WORDS);
+    for (int j = 0; j < T::WPER; ++j)
+      request_words(word_base[j] + (s & ~3), word_off[j], word_to[j] + ((s >> 2) & 1) * T::WORDS);
+  };
+  auto request = [&](int s, uint32_t slot, int from, int to) {  // lines from .. to - 1 of stage s
     const uint32_t d = lds0 + slot * STAGE + wave * (PER * 1024);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) request_lines(line_base[j] + (int64_t)s * ROW, line_off[j], d + j * 1024);
+    for (int j = 0; j < PER; ++j)
+      if (j >= from && j < to) request_lines(line_base[j] + (int64_t)s * ROW, line_off[j], d + j * 1024);
   };
 
   uint32_t sw, sx[FJ], sw_next, sx_next[FJ];
@@ -178,9 +180,9 @@ __global__ __launch_bounds__(64 * WM * WN, FI * FJ > 8 ? 1 : 2) void fp8_tile(Fp
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   // the matrix ops of one 64 of k, each x block's next bytes (of slot, k64) read behind them
-  // (past the last stage what the slot holds, which nothing uses); SEL: the
-  // stage's byte of the scale words
-  auto step = [&](auto sel, uint32_t slot, int k64) {
+  // (past the last stage what the slot holds, which nothing uses), and after x block j's behind(j);
+  // SEL: the stage's byte of the scale words
+  auto step = [&](auto sel, uint32_t slot, int k64, auto behind) {
     constexpr int SEL = decltype(sel)::value;
     const float fw = __uint_as_float(((sw >> (8 * SEL)) & 255u) << 23);
 #pragma unroll
@@ -207,6 +209,7 @@ __global__ __launch_bounds__(64 * WM * WN, FI * FJ > 8 ? 1 : 2) void fp8_tile(Fp
         }
       }
       x[j] = read32(ox, 32 * j);
+      behind(j);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -219,18 +222,25 @@ __global__ __launch_bounds__(64 * WM * WN, FI * FJ > 8 ? 1 : 2) void fp8_tile(Fp
   constexpr integral_constant<int, 1> s1{};
   constexpr integral_constant<int, 2> s2{};
   constexpr integral_constant<int, 3> s3{};
-  constexpr integral_constant<int, (SLOTS - 2) * PER> behind{};
+  constexpr integral_constant<int, (SLOTS - 2) * PER> in_flight{};
   auto next = [](uint32_t slot) { return slot + 1 == SLOTS ? 0u : slot + 1; };
   // stage s, in `slot`; req: stage s + SLOTS is there (and so are the ones before it); words: its scale words too
   auto stage = [&](auto sel, auto req, auto words, int s, uint32_t slot) {
-    step(sel, slot, 1);
+    step(sel, slot, 1, [](int) {});
     if constexpr (decltype(req)::value)
-      landed(behind);
+      landed(in_flight);
     else
       landed(s0);
     __builtin_amdgcn_s_barrier();
-    if constexpr (decltype(req)::value) request(words, s + SLOTS, slot);
-    step(sel, next(slot), 0);
+    // The largest tile's requests go out between the matrix ops, whose operands are here already (8192^3 429 ->
+    // 413 us); the others', which wait for memory rather than for the matrix cores, before them (128 x 128 tiles
+    // 65 against 67 us at 2047 x 2048 x 8512).
+    constexpr bool REQ = decltype(req)::value, BETWEEN = FJ >= 4;
+    if constexpr (REQ && decltype(words)::value) request_scales(s + SLOTS);
+    if constexpr (REQ && !BETWEEN) request(s + SLOTS, slot, 0, PER);
+    step(sel, next(slot), 0, [&](int j) {
+      if constexpr (REQ && BETWEEN) request(s + SLOTS, slot, PER * j / FJ, PER * (j + 1) / FJ);
+    });
   };
   auto take_scales = [&]() {
     sw = sw_next;
@@ -238,12 +248,13 @@ __global__ __launch_bounds__(64 * WM * WN, FI * FJ > 8 ? 1 : 2) void fp8_tile(Fp
     for (int j = 0; j < FJ; ++j) sx[j] = sx_next[j];
   };
 
-  request(std::true_type{}, 0, 0);
+  request_scales(0);
+  request(0, 0, 0, PER);
   landed(s0);
   __builtin_amdgcn_s_barrier();
 #pragma unroll
   for (int i = 1; i < SLOTS; ++i)
-    if (nk > i) request(std::false_type{}, i, i);
+    if (nk > i) request(i, i, 0, PER);
   read_scales(0);
   take_scales();
 #pragma unroll
