@@ -89,17 +89,49 @@ hxq::Fp8Plan plan(bool y_bf16, int64_t Mx, int64_t M, int64_t N, int64_t K, int6
   return p;
 }
 
-struct Workspace {
-  int64_t xq, xs, part, bytes;  // offsets, total
+// A product as it is launched: rows [0, cut) of y by `p`, the rest by `rest`
+// (cut == M: all by `p`).  A few tiles more than whole rounds of the largest
+// tiles over the CUs would take a round of their own; where they are at most
+// half a round, their rows go to smaller tiles in a second launch (2048 x
+// 11008 at 25600 rows, 800 tiles on 256 CUs: 537 -> 450 us).
+struct Plans {
+  hxq::Fp8Plan p, rest;
+  int64_t cut;
+  bool ok;
+  int64_t xq, xs, part, bytes;  // offsets in the workspace, its size
 };
-Workspace workspace_of(const hxq::Fp8Plan& p, int x_dtype, int64_t Mx, int64_t K) {
-  Workspace w = {};
-  if (x_dtype != HXQ_E4M3 && !p.converts) {
-    w.xs = round256(Mx * fp8_padded(K));
-    w.part = w.xs + round256(Mx * fp8_scale_row(K));
+Plans plans(int x_dtype, int y_dtype, int64_t Mx, int64_t M, int64_t N, int64_t K, int64_t E, bool experts, bool gather) {
+  const bool y_bf16 = y_dtype == HXQ_BF16;
+  Plans l = {};
+  l.p = plan(y_bf16, Mx, M, N, K, E, gather);
+  l.cut = M;
+  if (!experts && l.p.ok && l.p.kernel == hxq::kFp8Tile256) {
+    const int64_t cus = hxq::device_cu_count(), tiles = l.p.tiles_m * l.p.tiles_n, over = tiles % cus;
+    const int64_t main_m = tiles / cus * cus / l.p.tiles_n;
+    if (main_m > 0 && over > 0 && 2 * over <= cus) {
+      const hxq::Fp8Plan rest = plan(y_bf16, M - main_m * 256, M - main_m * 256, N, K, 1, false);
+      if (rest.ok && rest.kernel != hxq::kFp8Tile256) {
+        l.cut = main_m * 256;
+        l.p.tiles_m = main_m;
+        l.rest = rest;
+      }
+    }
   }
-  w.bytes = w.part + p.part_bytes;
-  return w;
+  l.ok = l.p.ok;
+  const bool converts = l.p.converts && l.cut == M;
+  if (x_dtype != HXQ_E4M3 && !converts) {
+    l.xs = round256(Mx * fp8_padded(K));
+    l.part = l.xs + round256(Mx * fp8_scale_row(K));
+  }
+  l.bytes = l.part + std::max(l.p.part_bytes, l.rest.part_bytes);
+  return l;
+}
+
+hipError_t launch(hxq::Fp8Args a, const hxq::Fp8Plan& p, hipStream_t stream) {
+  a.S = p.S;
+  a.kbs = p.kbs;
+  const hipError_t e = p.kernel == hxq::kFp8Skinny ? hxq::launch_fp8_skinny(a, p, stream) : hxq::launch_fp8_tile(a, p, stream);
+  return e == hipSuccess && p.S > 1 ? hxq::launch_fp8_sum(a, stream) : e;
 }
 
 hipError_t quant_rows(const void* x, int x_dtype, uint8_t* q, uint8_t* scales, int64_t M, int64_t K,
@@ -125,16 +157,15 @@ int product(const void* x, int x_dtype, const uint8_t* x_scales, const int32_t* 
     return HXQ_ERR_SHAPE;
   if (M == 0 || N == 0) return HXQ_OK;
   if (Mx == 0) return HXQ_ERR_SHAPE;
-  const hxq::Fp8Plan p = plan(y_dtype == HXQ_BF16, Mx, M, N, K, E, rows != nullptr);
-  if (!p.ok) return HXQ_ERR_SHAPE;
+  const Plans l = plans(x_dtype, y_dtype, Mx, M, N, K, E, offsets != nullptr, rows != nullptr);
+  if (!l.ok) return HXQ_ERR_SHAPE;
   if (!y) return HXQ_ERR_NULL;
   if (K > 0 && (!x || !wq || !w_scales || (x_dtype == HXQ_E4M3 && !x_scales))) return HXQ_ERR_NULL;
   if (misaligned(x, size_of(x_dtype)) || misaligned(wq, 16) || misaligned(w_scales, 4) || misaligned(x_scales, 4) ||
       misaligned(rows, 4) || misaligned(offsets, 4) || misaligned(bias, 4) || misaligned(y, size_of(y_dtype)) ||
       misaligned(workspace, 16))
     return HXQ_ERR_ALIGN;
-  const Workspace w = workspace_of(p, x_dtype, Mx, K);
-  if (w.bytes > 0 && (!workspace || workspace_bytes < w.bytes)) return HXQ_ERR_UNSUPPORTED;
+  if (l.bytes > 0 && (!workspace || workspace_bytes < l.bytes)) return HXQ_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   hxq::Fp8Args a = {};
   a.rows = rows;
@@ -144,42 +175,51 @@ int product(const void* x, int x_dtype, const uint8_t* x_scales, const int32_t* 
   a.bias = bias;
   a.y = y;
   a.y_bf16 = y_dtype == HXQ_BF16;
-  a.part = p.S > 1 ? reinterpret_cast<float*>(ws + w.part) : nullptr;
+  a.part = reinterpret_cast<float*>(at(ws, l.part));
   a.Mx = Mx;
-  a.M = (int)M;
+  a.M = (int)l.cut;
   a.N = (int)N;
   a.K = (int)K;
   a.Kp = (int)fp8_padded(K);
   a.Gs = (int)fp8_scale_row(K);
   a.E = (int)E;
-  a.S = p.S;
-  a.kbs = p.kbs;
-  (void)hipGetLastError();  // start from a clean error state
   a.x_dtype = HXQ_E4M3;
-  if (x_dtype != HXQ_E4M3 && p.converts) {
-    a.xf = x;
-    a.x_dtype = x_dtype;
-  } else if (x_dtype == HXQ_E4M3) {
+  (void)hipGetLastError();  // start from a clean error state
+  if (x_dtype == HXQ_E4M3) {
     a.x = static_cast<const uint8_t*>(x);
     a.xs = x_scales;
+  } else if (l.p.converts) {
+    a.xf = x;
+    a.x_dtype = x_dtype;
   } else if (K > 0) {
-    a.x = ws + w.xq;
-    a.xs = ws + w.xs;
-    const hipError_t e = quant_rows(x, x_dtype, ws + w.xq, ws + w.xs, Mx, K, stream);
-    if (e != hipSuccess) return HXQ_ERR_HIP;
+    a.x = ws + l.xq;
+    a.xs = ws + l.xs;
+    if (quant_rows(x, x_dtype, ws + l.xq, ws + l.xs, Mx, K, stream) != hipSuccess) return HXQ_ERR_HIP;
   }
-  hipError_t e = p.kernel == hxq::kFp8Skinny ? hxq::launch_fp8_skinny(a, p, stream) : hxq::launch_fp8_tile(a, p, stream);
-  if (e == hipSuccess && p.S > 1) e = hxq::launch_fp8_sum(a, stream);
+  hipError_t e = launch(a, l.p, stream);
+  if (e == hipSuccess && l.cut < M) {
+    a.x += l.cut * a.Kp;
+    a.xs += l.cut * a.Gs;
+    a.y = at(a.y, l.cut * N * (a.y_bf16 ? 2 : 4));
+    a.Mx = a.M = (int)(M - l.cut);
+    e = launch(a, l.rest, stream);
+  }
   return status_of(e);
 }
 
-int64_t product_workspace(int x_dtype, int64_t Mx, int64_t M, int64_t E, int64_t N, int64_t K) {
+int64_t product_workspace(int x_dtype, int64_t Mx, int64_t M, int64_t E, int64_t N, int64_t K, bool experts) {
   if (!float_dtype(x_dtype) && x_dtype != HXQ_E4M3) return HXQ_ERR_DTYPE;
   if (bad_dim(Mx) || bad_dim(M) || bad_dim(N) || bad_dim(K) || E < 1 || E > kMaxExperts) return HXQ_ERR_SHAPE;
   if (M == 0 || N == 0) return 0;
-  const hxq::Fp8Plan p = plan(false, Mx, M, N, K, E, true);
-  if (!p.ok || Mx == 0) return HXQ_ERR_SHAPE;
-  return workspace_of(p, x_dtype, Mx, K).bytes;
+  if (Mx == 0) return HXQ_ERR_SHAPE;
+  // enough for either type of y, with and without a gather
+  int64_t bytes = 0;
+  for (int i = 0; i < (experts ? 4 : 2); ++i) {
+    const Plans l = plans(x_dtype, i & 1 ? HXQ_BF16 : HXQ_F32, Mx, M, N, K, E, experts, i >= 2);
+    if (!l.ok) return HXQ_ERR_SHAPE;
+    bytes = std::max(bytes, l.bytes);
+  }
+  return bytes;
 }
 
 }  // namespace
@@ -219,7 +259,7 @@ int hxq_linear_fwd_fp8(const void* x, int x_dtype, const uint8_t* x_scales, cons
 }
 
 int64_t hxq_linear_fwd_fp8_workspace(int x_dtype, int64_t M, int64_t N, int64_t K) {
-  return product_workspace(x_dtype, M, M, 1, N, K);
+  return product_workspace(x_dtype, M, M, 1, N, K, false);
 }
 
 int hxq_linear_fwd_fp8_experts(const void* x, int x_dtype, const uint8_t* x_scales, const int32_t* rows,
@@ -233,7 +273,7 @@ int hxq_linear_fwd_fp8_experts(const void* x, int x_dtype, const uint8_t* x_scal
 }
 
 int64_t hxq_linear_fwd_fp8_experts_workspace(int x_dtype, int64_t M_x, int64_t M, int64_t E, int64_t N, int64_t K) {
-  return product_workspace(x_dtype, M_x, M, E, N, K);
+  return product_workspace(x_dtype, M_x, M, E, N, K, true);
 }
 
 int hxq_rms_norm(const void* x, int x_dtype, const void* residual, int residual_dtype, const float* weight, float eps,

@@ -58,8 +58,9 @@ __device__ __forceinline__ void request_words(const uint8_t* base, uint32_t off,
 }
 
 // WM x WN waves, each FJ blocks of 32 rows of x by FI blocks of 32 outputs; SLOTS stages in LDS.
-template <int WM, int WN, int FJ, int FI, int SLOTS>
+template <int WM_, int WN_, int FJ_, int FI_, int SLOTS_>
 struct TileShape {
+  static constexpr int WM = WM_, WN = WN_, FJ = FJ_, FI = FI_, SLOTS = SLOTS_;
   static constexpr int WAVES = WM * WN, TM = 32 * WM * FJ, TN = 32 * WN * FI;
   static constexpr int STAGE = (TM + TN) * ROW;
   static constexpr int PER = (TM + TN) / 8 / WAVES;  // line requests of a wave and stage
@@ -70,32 +71,13 @@ struct TileShape {
   static_assert(PER * 8 * WAVES == TM + TN && SLOTS <= 4 && LDS <= 160 * 1024, "tile shape");
 };
 
-template <bool WIDE, int WM, int WN, int FJ, int FI, int SLOTS>
-__global__ __launch_bounds__(64 * WM * WN, FI * FJ > 8 ? 1 : 2) void fp8_tile(Fp8Args a, int tiles_n, int tiles_m) {
-  using T = TileShape<WM, WN, FJ, FI, SLOTS>;
-  constexpr int TM = T::TM, TN = T::TN, STAGE = T::STAGE, PER = T::PER;
-  __shared__ __align__(1024) uint8_t lds[T::LDS];
+template <bool WIDE, class T>
+__device__ __forceinline__ void tile_body(const Fp8Args& a, uint8_t* lds, const RowTile t, const int n0, const int split) {
+  constexpr int WM = T::WM, FJ = T::FJ, FI = T::FI, SLOTS = T::SLOTS, TM = T::TM, STAGE = T::STAGE, PER = T::PER;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WM, wn = wave / WM;
   const int r32 = lane & 31, half = lane >> 5;
-
-  // tiles of eight row tiles (all of a column of them first) stay together on
-  // one XCD, which then shares their lines in its L2
-  const int total_m = a.offsets ? fp8_row_tiles(a, TM) : tiles_m;
-  const int64_t work = (int64_t)total_m * tiles_n * a.S;
-  if ((int64_t)blockIdx.x >= work) return;
-  const int per = (int)(work >> 3);
-  const int bx = blockIdx.x;
-  int L = bx < 8 * per ? (bx & 7) * per + (bx >> 3) : bx;
-  const int split = L / (total_m * tiles_n);
-  L -= split * (total_m * tiles_n);
-  const int group = L / (8 * tiles_n), in = L - group * 8 * tiles_n;
-  const int gm = min(8, total_m - 8 * group);
-  const int tn = in / gm, tm = 8 * group + in - tn * gm;
-  const RowTile t = fp8_row_tile(a, tm, TM);
-  if (t.rows <= 0) return;
-  const int n0 = tn * TN;
   const int nb = (a.N + 127) >> 7;
   const int kb0 = split * a.kbs, nk = min(a.kbs, (a.Kp >> 7) - kb0);  // the split's stages (kbs % 4 == 0 if split)
 
@@ -368,23 +350,50 @@ __global__ __launch_bounds__(64 * WM * WN, FI * FJ > 8 ? 1 : 2) void fp8_tile(Fp
   }
 }
 
-template <int WM, int WN, int FJ, int FI, int SLOTS>
-void tile_launch(const Fp8Args& a, const Fp8Plan& p, hipStream_t s) {
-  const dim3 grid((unsigned)(p.tiles_n * p.tiles_m * p.S)), block(64 * WM * WN);
-  if (p.wide)
-    hipLaunchKernelGGL((fp8_tile<true, WM, WN, FJ, FI, SLOTS>), grid, block, 0, s, a, (int)p.tiles_n, (int)p.tiles_m);
+// Tiles of T; one whose rows fit S's height (an expert's last, mostly) is done in that shape, with the matrix ops
+// of the rows it has.
+template <bool WIDE, class T, class S>
+__global__ __launch_bounds__(64 * T::WAVES, 2) void fp8_tile(Fp8Args a, int tiles_n, int tiles_m) {
+  static_assert(T::WAVES == S::WAVES && T::TN == S::TN, "one grid for both");
+  __shared__ __align__(1024) uint8_t lds[T::LDS > S::LDS ? T::LDS : S::LDS];
+  // tiles of eight row tiles (all of a column of them first) stay together on
+  // one XCD, which then shares their lines in its L2
+  const int total_m = a.offsets ? fp8_row_tiles(a, T::TM) : tiles_m;
+  const int64_t work = (int64_t)total_m * tiles_n * a.S;
+  if ((int64_t)blockIdx.x >= work) return;
+  const int per = (int)(work >> 3);
+  const int bx = blockIdx.x;
+  int L = bx < 8 * per ? (bx & 7) * per + (bx >> 3) : bx;
+  const int split = L / (total_m * tiles_n);
+  L -= split * (total_m * tiles_n);
+  const int group = L / (8 * tiles_n), in = L - group * 8 * tiles_n;
+  const int gm = min(8, total_m - 8 * group);
+  const int tn = in / gm, tm = 8 * group + in - tn * gm;
+  const RowTile t = fp8_row_tile(a, tm, T::TM);
+  if (t.rows <= 0) return;
+  if (T::TM != S::TM && t.rows <= S::TM)
+    tile_body<WIDE, S>(a, lds, t, tn * T::TN, split);
   else
-    hipLaunchKernelGGL((fp8_tile<false, WM, WN, FJ, FI, SLOTS>), grid, block, 0, s, a, (int)p.tiles_n, (int)p.tiles_m);
+    tile_body<WIDE, T>(a, lds, t, tn * T::TN, split);
+}
+
+template <class T, class S = T>
+void tile_launch(const Fp8Args& a, const Fp8Plan& p, hipStream_t s) {
+  const dim3 grid((unsigned)(p.tiles_n * p.tiles_m * p.S)), block(64 * T::WAVES);
+  if (p.wide)
+    hipLaunchKernelGGL((fp8_tile<true, T, S>), grid, block, 0, s, a, (int)p.tiles_n, (int)p.tiles_m);
+  else
+    hipLaunchKernelGGL((fp8_tile<false, T, S>), grid, block, 0, s, a, (int)p.tiles_n, (int)p.tiles_m);
 }
 
 }  // namespace
 
 hipError_t launch_fp8_tile(const Fp8Args& a, const Fp8Plan& p, hipStream_t s) {
   switch (p.kernel) {
-    case kFp8Tile32: tile_launch<1, 2, 1, 1, 3>(a, p, s); break;
-    case kFp8Tile64: tile_launch<2, 4, 1, 1, 3>(a, p, s); break;
-    case kFp8Tile128: tile_launch<2, 2, 2, 2, 2>(a, p, s); break;
-    default: tile_launch<2, 4, 4, 2, 2>(a, p, s); break;
+    case kFp8Tile32: tile_launch<TileShape<1, 2, 1, 1, 3>>(a, p, s); break;
+    case kFp8Tile64: tile_launch<TileShape<2, 4, 1, 1, 3>>(a, p, s); break;
+    case kFp8Tile128: tile_launch<TileShape<2, 2, 2, 2, 2>, TileShape<1, 4, 2, 1, 3>>(a, p, s); break;
+    default: tile_launch<TileShape<2, 4, 4, 2, 2>, TileShape<1, 8, 4, 1, 3>>(a, p, s); break;
   }
   return hipGetLastError();
 }
