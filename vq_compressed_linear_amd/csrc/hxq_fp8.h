@@ -80,7 +80,7 @@ struct Fp8Plan {
   int kernel;       // one of Fp8Kernel
   bool wide;        // operands widened to bf16 (tile kernels)
   bool converts;    // the kernel converts a float32 or bf16 x itself
-  int waves;        // waves that share a tile's sum (skinny kernels)
+  int waves, depth; // skinny kernel: waves that share a tile's sum, blocks of a wave in flight
   int S, kbs;
   int64_t tiles_m, tiles_n;
   int64_t part_bytes;

@@ -68,14 +68,20 @@ hxq::Fp8Plan plan(bool y_bf16, int64_t Mx, int64_t M, int64_t N, int64_t K, int6
   else
     p.kernel = hxq::kFp8Tile32;
   const bool skinny = p.kernel == hxq::kFp8Skinny;
-  p.waves = blocks >= 32 ? 8 : 4;
   p.tiles_n = (N + kTileOutputs[p.kernel] - 1) / kTileOutputs[p.kernel];
   p.tiles_m = tiles_m(p.kernel);
   const int64_t wgs = p.tiles_n * p.tiles_m;
-  if (skinny)
-    p.S = wgs < cus && blocks >= 4 * p.waves ? (int)std::min<int64_t>((2 * cus + wgs - 1) / wgs, blocks / (2 * p.waves)) : 1;
-  else
-    p.S = (int)splits(p.kernel);
+  p.S = (int)splits(p.kernel);
+  if (skinny) {
+    // Few workgroups share the sum between more waves (2048 x 2048 at one row: 4.3 us in 8 waves, 6.3 in two
+    // splits of 4 waves, whose parts take a second launch), and between workgroups as well where it is long
+    // (2048 x 11008: 10.8 us in splits, 13.4 without; 2048 x 4096: 7.0, 5.7).
+    p.S = wgs < cus && blocks >= 48 ? (int)std::min<int64_t>((2 * cus + wgs - 1) / wgs, blocks / 16) : 1;
+    p.waves = wgs >= 2 * cus || blocks < 16 ? 4 : p.S > 1 || wgs >= cus || blocks < 32 ? 8 : 16;
+    // many workgroups: two blocks of each wave in flight (22016 x 2048: 10.8 against 11.5 us), else one, which
+    // leaves room for more waves (8512 x 2048: 6.4 against 7.0)
+    p.depth = wgs > 4 * cus ? 2 : 1;
+  }
   p.kbs = (int)((blocks + p.S - 1) / p.S);
   if (p.S > 1 && !skinny) p.kbs = (p.kbs + 3) / 4 * 4;  // whole words of scales
   if (p.kbs > 0) p.S = (int)((blocks + p.kbs - 1) / p.kbs);

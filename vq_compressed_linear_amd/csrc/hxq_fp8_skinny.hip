@@ -30,13 +30,12 @@ namespace hxq {
 
 namespace {
 
-// XT: -1 (x is e4m3), or the type of the values that the workgroup converts
+// DEPTH: blocks of a wave in flight.  XT: -1 (x is e4m3), or the type of the values that the workgroup converts
 // for itself (hxq_quant_fp8's arithmetic), into LDS: [16 rows][the split's
 // bytes], then the scales.  That saves a launch where x is small (measured:
 // one token through 22016 x 2048 and 2048 x 2048).
-template <int WAVES, int XT>
+template <int WAVES, int XT, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void fp8_skinny(Fp8Args a, int tiles_n, int tiles_m) {
-  constexpr int DEPTH = 4;  // blocks of a wave in flight
   __shared__ float red[WAVES][16][16];
   extern __shared__ __align__(16) uint8_t xlds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -163,22 +162,29 @@ __global__ __launch_bounds__(256) void fp8_sum(Fp8Args a) {
   }
 }
 
-template <int WAVES>
+template <int WAVES, int DEPTH>
 void skinny_launch(const Fp8Args& a, const Fp8Plan& p, hipStream_t s) {
   const dim3 grid((unsigned)(p.tiles_n * p.tiles_m * p.S)), block(64 * WAVES);
   const int lds = (a.M < 16 ? a.M : 16) * a.kbs * 129 + 15;
   if (a.x_dtype == kF32)
-    hipLaunchKernelGGL((fp8_skinny<WAVES, kF32>), grid, block, lds, s, a, (int)p.tiles_n, (int)p.tiles_m);
+    hipLaunchKernelGGL((fp8_skinny<WAVES, kF32, DEPTH>), grid, block, lds, s, a, (int)p.tiles_n, (int)p.tiles_m);
   else if (a.x_dtype == kBf16)
-    hipLaunchKernelGGL((fp8_skinny<WAVES, kBf16>), grid, block, lds, s, a, (int)p.tiles_n, (int)p.tiles_m);
+    hipLaunchKernelGGL((fp8_skinny<WAVES, kBf16, DEPTH>), grid, block, lds, s, a, (int)p.tiles_n, (int)p.tiles_m);
   else
-    hipLaunchKernelGGL((fp8_skinny<WAVES, -1>), grid, block, 0, s, a, (int)p.tiles_n, (int)p.tiles_m);
+    hipLaunchKernelGGL((fp8_skinny<WAVES, -1, DEPTH>), grid, block, 0, s, a, (int)p.tiles_n, (int)p.tiles_m);
 }
 
 }  // namespace
 
 hipError_t launch_fp8_skinny(const Fp8Args& a, const Fp8Plan& p, hipStream_t s) {
-  p.waves == 4 ? skinny_launch<4>(a, p, s) : skinny_launch<8>(a, p, s);
+  if (p.depth == 2)  // (many workgroups: four waves each)
+    skinny_launch<4, 2>(a, p, s);
+  else if (p.waves == 4)
+    skinny_launch<4, 1>(a, p, s);
+  else if (p.waves == 8)
+    skinny_launch<8, 1>(a, p, s);
+  else
+    skinny_launch<16, 1>(a, p, s);
   return hipGetLastError();
 }
 
