@@ -430,7 +430,7 @@ int hxq_select_variant(int fmt_pk12, int x_dtype, int64_t M, int64_t N, int64_t 
  * Layouts (all contiguous)
  *   - values: e4m3 bytes (OCP: largest 448, 0x7f / 0xff NaN, no infinities),
  *     rows padded with zeros to Kp = 128 * ceil(K / 128) columns.
- *   - scales: e8m0 bytes b, standing for 2^(b - 127).  Activations [M][Kp]
+ *   - scales: e8m0 bytes b, 1 to 254, standing for 2^(b - 127).  Activations [M][Kp]
  *     have one for each 128 columns of a row, [M][Gs]; weights [N][Kp] one for
  *     each 128 x 128 block, [ceil(N / 128)][Gs].  Gs = 4 * ceil(K / 512): rows
  *     of scales are padded to a multiple of 4 with 127 (one).
@@ -481,10 +481,11 @@ int hxq_quant_fp8_weight(const void* w, int w_dtype, uint8_t* q, uint8_t* scales
  *             at once need one each, captured graphs among them.
  * Arithmetic: with float32 y the 8-bit values are multiplied exactly and
  * summed in fp32 (widened to bf16, on the bf16 matrix cores).  With bf16 y
- * past 64 rows the 8-bit matrix cores may multiply, at twice the rate: they
- * keep a product only down to 2^-13 of the largest of its group of 8 (1.5e-5
- * of the result, measured; bf16's own rounding is 2^-9 of it).  Partial sums
- * are added in a fixed order; bf16 y is rounded once.  A NaN in x makes its
+ * the 8-bit matrix cores may multiply, at twice the rate: they keep a product
+ * only down to 2^-13 of the largest of its group of 8 (1.5e-5 of the result,
+ * measured; bf16's own rounding is 2^-9 of it).  Partial sums are added in a
+ * fixed order; bf16 y is rounded once.  A row's result depends on the sizes
+ * of the call (they choose the kernel), not on the other rows' values.  A NaN in x makes its
  * whole row of y NaN and no other.  K == 0: y = bias (or 0).
  * Errors: HXQ_ERR_DTYPE; HXQ_ERR_SHAPE (also more than 2^22 tiles of y);
  * HXQ_ERR_NULL; HXQ_ERR_ALIGN; HXQ_ERR_UNSUPPORTED for a workspace smaller

@@ -285,15 +285,19 @@ def test_experts_deterministic_with_a_split_sum():
     near(out[0][:5], Y, 1e-5 * B + U * np.abs(Y))
 
 
-def test_experts_bad_indices_stay_inside():
+@pytest.mark.parametrize("M", [9, 300, 3000])
+@pytest.mark.parametrize("y_dtype", [F32, BF16])
+def test_experts_bad_indices_stay_inside(M, y_dtype):
     """Rows out of range and offsets that break their rule: unspecified values, no access outside."""
-    x, (q, s) = make(1, 6, 256), weight8(make(2, 4, 64, 256))
-    guard = torch.full((20 + 9 + 20, 64), 7.0, device="cuda")
-    y = guard[20:29]
-    rows = torch.tensor([0, -1, 2**31 - 1, -(2**31), 6, 5, 3, 2, 1], dtype=torch.int32, device="cuda")
-    for off in ([0, 3, 5, 7, 9], [0, 100, 2**31 - 1, 5, 9], [-5, 4, -(2**31), 9, 9], [9, 7, 5, 3, 0], [3, 3, 3, 3, 3]):
+    x, (q, s) = make(1, 6, 256), weight8(make(2, 4, 256, 256))
+    guard = torch.full((20 + M + 20, 256), 7.0, dtype=y_dtype, device="cuda")
+    y = guard[20:20 + M]
+    rows = torch.arange(M, dtype=torch.int32, device="cuda") % 6
+    rows[:8] = torch.tensor([0, -1, 2**31 - 1, -(2**31), 6, 5, 3, 2], dtype=torch.int32, device="cuda")
+    for off in ([0, 3, 5, 7, 9], [0, 100, 2**31 - 1, 5, 9], [-5, 4, -(2**31), 9, 9], [9, 7, 5, 3, 0], [3, 3, 3, 3, 3],
+                [2**31 - 1, 0, 2**31 - 1, 0, 2**31 - 1]):
         hx.hxq_linear_fwd_fp8_experts(x, None, rows, torch.tensor(off, dtype=torch.int32, device="cuda"), q, s, None, y)
-    assert (guard[:20] == 7.0).all() and (guard[29:] == 7.0).all()
+    assert (guard[:20] == 7.0).all() and (guard[20 + M:] == 7.0).all()
 
 
 # ------------------------------------------------------------------------ norm

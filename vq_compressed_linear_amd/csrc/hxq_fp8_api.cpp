@@ -57,7 +57,7 @@ hxq::Fp8Plan plan(bool y_bf16, int64_t Mx, int64_t M, int64_t N, int64_t K, int6
   };
   auto fills = [&](int k) { return 10 * tiles(k) * splits(k) >= 6 * cus; };
   const bool near32 = K > 0 && (gather ? Mx : 256) * Kp < ((int64_t)1 << 32) && Kp < ((int64_t)1 << 24);
-  if (!near32 || each <= (E > 1 ? 1 : 8) || (each <= 128 && tiles(hxq::kFp8Skinny) * blocks <= 32 * cus))
+  if (!near32 || each <= (E > 1 ? 1 : 8) || (each <= 128 && tiles(hxq::kFp8Skinny) <= 32 * cus / std::max<int64_t>(1, blocks)))
     p.kernel = hxq::kFp8Skinny;
   else if (each >= 192 && fills(hxq::kFp8Tile256))
     p.kernel = hxq::kFp8Tile256;
@@ -89,7 +89,7 @@ hxq::Fp8Plan plan(bool y_bf16, int64_t Mx, int64_t M, int64_t N, int64_t K, int6
   // A small x is converted by every workgroup for itself instead of in a launch before: through 22016 x 2048
   // 11.4 against 13.5 us for one row, 13.9 against 14.6 for three, 15.3 against 15.0 for four; one row through
   // 2048 x 11008 (split) 10.8 against 12.3.  At most 16 rows of the split's bytes lie in LDS.
-  p.converts = skinny && K > 0 && Mx * p.kbs * 128 <= 6144 && std::min<int64_t>(M, 16) * p.kbs * 129 <= 48 * 1024;
+  p.converts = skinny && K > 0 && Mx * p.kbs * 128 <= 6144 && std::min<int64_t>(M, 16) * p.kbs * 129 <= 40 * 1024;
   p.ok = p.tiles_n <= kMaxTiles && p.tiles_m <= kMaxTiles && p.tiles_n * p.tiles_m * p.S <= kMaxTiles;
   p.part_bytes = p.ok && p.S > 1 ? p.S * M * N * 4 : 0;
   return p;

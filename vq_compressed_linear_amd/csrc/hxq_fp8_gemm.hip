@@ -358,7 +358,7 @@ __global__ __launch_bounds__(64 * T::WAVES, 2) void fp8_tile(Fp8Args a, int tile
   __shared__ __align__(1024) uint8_t lds[T::LDS > S::LDS ? T::LDS : S::LDS];
   // tiles of eight row tiles (all of a column of them first) stay together on
   // one XCD, which then shares their lines in its L2
-  const int total_m = a.offsets ? fp8_row_tiles(a, T::TM) : tiles_m;
+  const int total_m = a.offsets ? fp8_row_tiles(a, T::TM, tiles_m) : tiles_m;
   const int64_t work = (int64_t)total_m * tiles_n * a.S;
   if ((int64_t)blockIdx.x >= work) return;
   const int per = (int)(work >> 3);

@@ -23,6 +23,8 @@ __device__ __forceinline__ int fp8_rows_end(const Fp8Args& a) { return a.offsets
 // Tile t of height tm over the rows: without experts rows t tm .. + tm - 1,
 // else the t-th tile when each expert's rows are cut into tiles of their own.
 // Found by every wave for itself: the 64 lanes look at 64 experts at a time.
+// (Counts are kept below 2^30, past the 2^22 tiles of a launch, so that offsets
+// that break their contract cannot overflow them.)
 __device__ __forceinline__ RowTile fp8_row_tile(const Fp8Args& a, int t, int tm) {
   if (!a.offsets) return {0, t * tm, min(tm, a.M - t * tm)};
   const int lane = lane_id();
@@ -31,7 +33,7 @@ __device__ __forceinline__ RowTile fp8_row_tile(const Fp8Args& a, int t, int tm)
     const int e = min(e0 + lane, a.E - 1);
     const int lo = fp8_offset(a, e), hi = fp8_offset(a, e + 1);
     const int rows = e0 + lane < a.E ? max(hi - lo, 0) : 0;
-    const int tiles = (int)(((int64_t)rows + tm - 1) / tm);
+    const int tiles = min((int)(((int64_t)rows + tm - 1) / tm), 1 << 23);
     int incl = tiles;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
@@ -46,16 +48,19 @@ __device__ __forceinline__ RowTile fp8_row_tile(const Fp8Args& a, int t, int tm)
       const int n = __builtin_amdgcn_readlane(rows, l) - r;
       return {e0 + l, __builtin_amdgcn_readlane(lo, l) + r, min(n, tm)};
     }
-    before += __builtin_amdgcn_readlane(incl, kWave - 1);
+    before = min(before + __builtin_amdgcn_readlane(incl, kWave - 1), 1 << 29);
   }
   return {0, 0, 0};
 }
 
-// How many such tiles there are.
-__device__ __forceinline__ int fp8_row_tiles(const Fp8Args& a, int tm) {
+// How many such tiles there are, at most `most`.
+__device__ __forceinline__ int fp8_row_tiles(const Fp8Args& a, int tm, int most) {
   int n = 0;
-  for (int e = lane_id(); e < a.E; e += kWave) n += (int)(((int64_t)max(fp8_offset(a, e + 1) - fp8_offset(a, e), 0) + tm - 1) / tm);
-  return wave_sum_dpp_i(n);
+  for (int e = lane_id(); e < a.E; e += kWave) {
+    const int rows = max(fp8_offset(a, e + 1) - fp8_offset(a, e), 0);
+    n = min(n + min((int)(((int64_t)rows + tm - 1) / tm), most), most);
+  }
+  return min(wave_sum_dpp_i(n), most);  // most <= 2^22: 64 of them fit
 }
 
 // The expert of row m (m < fp8_rows_end): the last e with offset(e) <= m.
