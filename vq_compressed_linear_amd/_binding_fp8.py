@@ -11,6 +11,7 @@ library is reached; nothing is computed here.
 from __future__ import annotations
 
 import contextlib
+import functools
 
 import torch
 
@@ -78,6 +79,13 @@ def _stream(stream, dev: int):
     if stream is None and _raw_stream is not None:
         return _raw_stream(dev)
     return B._stream(stream, dev)
+
+
+@functools.lru_cache(maxsize=4096)
+def _need(dev: int, query: str, *sizes) -> int:
+    """A workspace query's answer for the device (it depends on nothing else)."""
+    with _on(dev):
+        return getattr(B.lib(), query)(*sizes)
 
 
 def _workspace(workspace, need: int, what: str, dev: int, stream):
@@ -173,7 +181,7 @@ def hxq_linear_fwd_fp8(x, x_scales, wq, w_scales, bias, y, stream=None, workspac
     dev = _device(x, x_scales, wq, w_scales, bias, y, workspace)
     lib = B.lib()
     with _on(dev):
-        ptr, size, keep = _workspace(workspace, lib.hxq_linear_fwd_fp8_workspace(dt, M, N, K),
+        ptr, size, keep = _workspace(workspace, _need(dev, "hxq_linear_fwd_fp8_workspace", dt, M, N, K),
                                      "hxq_linear_fwd_fp8_workspace", dev, stream)
         st = lib.hxq_linear_fwd_fp8(x.data_ptr(), dt, B._ptr(x_scales), wq.data_ptr(), w_scales.data_ptr(),
                                     B._ptr(bias), y.data_ptr(), ydt, M, N, K, ptr, size, _stream(stream, dev))
@@ -205,7 +213,7 @@ def hxq_linear_fwd_fp8_experts(x, x_scales, rows, offsets, wq, w_scales, bias, y
     dev = _device(x, x_scales, rows, offsets, wq, w_scales, bias, y, workspace)
     lib = B.lib()
     with _on(dev):
-        ptr, size, keep = _workspace(workspace, lib.hxq_linear_fwd_fp8_experts_workspace(dt, Mx, M, E, N, K),
+        ptr, size, keep = _workspace(workspace, _need(dev, "hxq_linear_fwd_fp8_experts_workspace", dt, Mx, M, E, N, K),
                                      "hxq_linear_fwd_fp8_experts_workspace", dev, stream)
         st = lib.hxq_linear_fwd_fp8_experts(x.data_ptr(), dt, B._ptr(x_scales), B._ptr(rows), offsets.data_ptr(),
                                             wq.data_ptr(), w_scales.data_ptr(), B._ptr(bias), y.data_ptr(), ydt, Mx,
@@ -269,7 +277,7 @@ def hxq_rms_norm_bwd(dy, h, weight, rstd, dx, dweight=None, dresidual=None, stre
     dev = _device(dy, h, weight, rstd, dx, dweight, dresidual, workspace)
     lib = B.lib()
     with _on(dev):
-        need = 0 if dweight is None else lib.hxq_rms_norm_bwd_workspace(M, K)
+        need = 0 if dweight is None else _need(dev, "hxq_rms_norm_bwd_workspace", M, K)
         ptr, size, keep = _workspace(workspace, need, "hxq_rms_norm_bwd_workspace", dev, stream)
         st = lib.hxq_rms_norm_bwd(dy.data_ptr(), dt, h.data_ptr(), hdt, B._ptr(weight), rstd.data_ptr(),
                                   B._ptr(dresidual), dx.data_ptr(), B._ptr(dweight), M, K, ptr, size,
