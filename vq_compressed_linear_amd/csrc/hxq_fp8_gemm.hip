@@ -1,11 +1,12 @@
-// Block-scaled 8-bit product for many rows of x: 256 x 256 tiles of y, one
-// layer or one per expert.
+// Block-scaled 8-bit product for more than a few rows of x: tiles of y staged
+// through LDS, one layer or one per expert.
 //
 //     y[m][n] = bias[n] + sum_k (qx[m][k] px[m][k / 128]) (qw[n][k] pw[n / 128][k / 128])
 //
-// Eight waves, two to a SIMD, each own 128 rows of x by 64 outputs: eight
-// accumulators of 32 x 32, the weight as the A operand (so a lane holds runs
-// of four outputs of one row of y).  Two forms:
+// Shapes (rows of x x outputs): 32 x 64 (2 waves), 64 x 128 (8), 128 x 128 (4)
+// and 256 x 256 (8).  A wave owns FJ x FI blocks of 32 x 32, the weight as the
+// A operand (so a lane holds runs of four outputs of one row of y).  In two
+// forms:
 //   - bf16 y: v_mfma_scale_f32_32x32x64_f8f6f4 on the bytes as they are, which
 //     takes both operands' powers of two;
 //   - float32 y (WIDE): the bytes widened to bf16 with their power of two
@@ -13,8 +14,20 @@
 //     a product only down to 2^-13 of the largest in its group of 8.  Half the
 //     matrix rate.
 //
-// A stage is 128 of k: one cache line of each of the tile's 512 operand rows,
-// 64 KB of LDS, two stages in it.  Lines go from memory straight to LDS
+// Bound: the matrix cores for the large tiles, the weight's bytes for the small
+// ones.  Measured: 8192^3 in 407-430 us with bf16 y (2.55-2.7 PFLOP/s), 740-755
+// us with float32 y (1.46-1.49); gate|up (22016 x 2048) at 2048 rows 96 us with
+// bf16 y; 64 experts of 2048 x 2048 with 8 rows each 52 us from memory (5.1
+// TB/s).  In the large tile the matrix cores are busy for 71% of the CUs' time
+// at 8192^3 (64 stages) and 45% at 16 stages, where a tile's start and its
+// output (every CU stores 128 KB at once) take about 8 us of 32.  No LDS bank
+// conflicts.  Four waves of 128 x 128 instead of eight of 128 x 64 read a third
+// less LDS but leave nothing to run behind a wait (8192^3 485 us); rings of four
+// to seven stages gained nothing for the small tiles; s_setprio around the
+// matrix ops cost 1-2%.
+//
+// A stage is 128 of k: one cache line of each of the tile's operand rows (64 KB
+// of LDS for the largest tile), SLOTS stages in a ring.  Lines go from memory straight to LDS
 // (global_load_lds_dwordx4, 8 lines to a wave instruction).  Piece c (16
 // bytes) of row r is kept at position c ^ ((r >> 1) & 7) of the row: then any
 // 16 lanes that read one piece of 16 consecutive rows touch every LDS bank
@@ -24,8 +37,10 @@
 //   - wait until this wave's part of stage s + 1 has landed and its reads of
 //     stage s are back; barrier (the one barrier of a stage: after it stage
 //     s + 1 is whole and no wave reads stage s any more);
-//   - the matrix ops of the second half, while stage s + 2 is requested into
-//     the slot of stage s and the first operands of stage s + 1 are read.
+//   - the matrix ops of the second half, while stage s + SLOTS is requested
+//     into the slot of stage s and the first operands of stage s + 1 are read.
+// Scales travel the same way, as words of four stages' bytes, every fourth
+// stage.
 // The requests are inline assembly: known to the compiler, every later read of
 // LDS would wait for all of them.  They name no register that they write.
 

@@ -13,6 +13,11 @@
 // a thread, from the sum of squares to the store.  A 128-column group is then
 // held by 16 lanes of one DPP row, whose largest magnitude needs no LDS.
 // Rows wider than 12288 columns are read a second time (from the caches).
+//
+// Measured: the norm of 25600 rows of 2048 (float32 x, bf16 residual, e4m3 out)
+// 84 us, 5.6 TB/s; one row 2.8 us; the gradient of 2047 rows of 4096 with the
+// weight's 24.8 + 4.2 us (4.7 TB/s in the first launch); conversion of 25600
+// rows of 11008 from bf16 156 us, 5.4 TB/s (a large copy: 4.9 TB/s).
 
 #include "hxq_fp8.h"
 #include "hxq_fp8_device.h"
@@ -138,11 +143,11 @@ __global__ __launch_bounds__(256) void rms_norm_rows(NormArgs a) {
 template <int XT, int RT, int OT>
 void norm_launch(const NormArgs& a, hipStream_t s) {
   const int K = a.K;
+  // A wave to a short row (25600 x 512: 21 us, 32 with a workgroup), else a workgroup: a wave with four chunks of
+  // a row of 2048 took 92 us against 84 at 25600 rows, 8.3 against 3.8 at 256.
   const unsigned rows = (unsigned)a.M, rows4 = (unsigned)((a.M + 3) / 4);
   if (K <= 512)
     hipLaunchKernelGGL((rms_norm_rows<64, 1, XT, RT, OT>), dim3(rows4), dim3(256), 0, s, a);
-  else if (K <= 2048 && a.M >= 2048)
-    hipLaunchKernelGGL((rms_norm_rows<64, 4, XT, RT, OT>), dim3(rows4), dim3(256), 0, s, a);
   else if (K <= 2048)
     hipLaunchKernelGGL((rms_norm_rows<256, 1, XT, RT, OT>), dim3(rows), dim3(256), 0, s, a);
   else if (K <= 4096)
@@ -330,16 +335,17 @@ __global__ __launch_bounds__(1024) void norm_dw_sum(const float* part, float* dw
   dw[o] = sum;
 }
 
-bool bwd_waves(int64_t K) { return K <= 2048; }  // a wave to a row, else a workgroup
+// A wave to a short row, else a workgroup (20000 x 2048: 83 us, 96 with a wave to a row).
+bool bwd_waves(int64_t K) { return K <= 512; }
 
 template <int DT, int HT>
 void norm_bwd_launch(const NormBwdArgs& a, hipStream_t s) {
   const int K = a.K;
   const dim3 grid((unsigned)norm_bwd_parts(a.M, K));
-  if (K <= 512)
+  if (bwd_waves(K))
     hipLaunchKernelGGL((rms_norm_bwd_rows<64, 1, DT, HT>), grid, dim3(256), 0, s, a);
-  else if (bwd_waves(K))
-    hipLaunchKernelGGL((rms_norm_bwd_rows<64, 4, DT, HT>), grid, dim3(256), 0, s, a);
+  else if (K <= 2048)
+    hipLaunchKernelGGL((rms_norm_bwd_rows<256, 1, DT, HT>), grid, dim3(256), 0, s, a);
   else if (K <= 4096)
     hipLaunchKernelGGL((rms_norm_bwd_rows<256, 2, DT, HT>), grid, dim3(256), 0, s, a);
   else if (K <= 12288)

@@ -21,6 +21,11 @@
 // loads in flight, and add their parts in wave order through LDS.  A sum that
 // is split over workgroups as well leaves its parts in the workspace for
 // fp8_sum.
+//
+// Measured, one row of x (bf16, converted in the kernel), weights rotating
+// through memory: 22016 x 2048 in 10.5 us (4.3 TB/s; a plain read of those
+// bytes takes 8.8), 8512 x 2048 6.4, 2048 x 2048 4.4, 2048 x 11008 10.2 (two
+// launches); 8 experts of 64, 2048 x 2048 each, 9.6 us.
 
 #include "hxq_fp8.h"
 #include "hxq_fp8_device.h"
