@@ -246,12 +246,14 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, uint8_t* lds, const 
   };
 
   request_scales(0);
-  request(0, 0, 0, PER);
-  landed(s0);
-  __builtin_amdgcn_s_barrier();
 #pragma unroll
-  for (int i = 1; i < SLOTS; ++i)
+  for (int i = 0; i < SLOTS; ++i)
     if (nk > i) request(i, i, 0, PER);
+  if (nk >= SLOTS)
+    landed(integral_constant<int, (SLOTS - 1) * PER>{});  // stage 0 and its scales
+  else
+    landed(s0);
+  __builtin_amdgcn_s_barrier();
   read_scales(0);
   take_scales();
 #pragma unroll
