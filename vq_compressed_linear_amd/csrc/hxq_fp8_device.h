@@ -110,6 +110,20 @@ __device__ __forceinline__ void store_row8(void* base, int64_t row0, int col, in
   }
 }
 
+// The same for float32, past the caches.
+__device__ __forceinline__ void stream_row8(float* base, int64_t row0, int col, int K, const float (&v)[8]) {
+  typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
+  float* p = base + row0 + col;
+  if (col + 8 <= K) {
+    __builtin_nontemporal_store(vec{v[0], v[1], v[2], v[3]}, reinterpret_cast<vec*>(p));
+    __builtin_nontemporal_store(vec{v[4], v[5], v[6], v[7]}, reinterpret_cast<vec*>(p + 4));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < K) p[i] = v[i];
+  }
+}
+
 // The e8m0 byte of the smallest power of two p >= 2^-126 with a <= 448 p, for
 // the bit pattern of a finite a >= 0: 448 = 1.75 * 2^8, so the exponent field
 // less 8, one more where the mantissa passes 1.75 (the addition then carries).

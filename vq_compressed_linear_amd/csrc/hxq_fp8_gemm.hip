@@ -330,7 +330,9 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, uint8_t* lds, const 
           if (bias)
 #pragma unroll
             for (int z = 0; z < 4; ++z) v[z] += bias[n + z];
-          *reinterpret_cast<f32x4*>(yf + (int64_t)(t.row0 + m0 + r) * a.N + n) = v;
+          // stored past the caches, which hold the operands that the tiles still to come share (experts with 64 rows
+          // each, float32 y, 77 -> 67 us; 512 rows of gate|up, bf16 y, 32.4 -> 29.6; split sums gain as well)
+          __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(yf + (int64_t)(t.row0 + m0 + r) * a.N + n));
         }
       }
     } else if (vec) {
@@ -344,9 +346,9 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, uint8_t* lds, const 
           if (bias)
 #pragma unroll
             for (int z = 0; z < 4; ++z) v[z] += bias[n + z], u[z] += bias[n + 4 + z];
-          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.y) + (int64_t)(t.row0 + m0 + r) * a.N + n) =
-              u32x4{f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16), f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16),
-                    f32_to_bf16_rne(u[0]) | (f32_to_bf16_rne(u[1]) << 16), f32_to_bf16_rne(u[2]) | (f32_to_bf16_rne(u[3]) << 16)};
+          const u32x4 o = {f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16), f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16),
+                           f32_to_bf16_rne(u[0]) | (f32_to_bf16_rne(u[1]) << 16), f32_to_bf16_rne(u[2]) | (f32_to_bf16_rne(u[3]) << 16)};
+          __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.y) + (int64_t)(t.row0 + m0 + r) * a.N + n));
         }
       }
     } else {

@@ -241,7 +241,7 @@ __global__ __launch_bounds__(256) void rms_norm_bwd_rows(NormBwdArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] += s[i];
           }
-          store_row8<kF32>(a.dx, row0, col, K, o);
+          stream_row8(a.dx, row0, col, K, o);  // (20000 x 2048: 83 -> 69 us)
         }
       }
     }
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(256) void rms_norm_bwd_rows(NormBwdArgs a) {
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = r * (d[i] * w[i] - h[i] * f) + s[i];
-        store_row8<kF32>(a.dx, row0, col, K, o);
+        stream_row8(a.dx, row0, col, K, o);
       }
     }
   }
