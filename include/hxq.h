@@ -219,10 +219,11 @@ int hxq_stream_read(const void* src, int64_t bytes, uint32_t* sink, int sink_wor
 int hxq_stream_read_nt(const void* src, int64_t bytes, uint32_t* sink, int sink_words,
                        hipStream_t stream);
 
-/* Measurement helper, not part of the forward pass: the dense bf16 weight of
- * one layer, for timing the buffered design the HXQ whitepaper's inference
- * paragraph describes (gather the weight into a shared bf16 buffer, then a
- * library matmul) against the fused kernels, which never form it.
+/* Helper, not part of the forward pass: the dense bf16 weight of one layer,
+ * for timing the buffered design the HXQ whitepaper's inference paragraph
+ * describes (gather the weight into a shared bf16 buffer, then a library
+ * matmul) against the fused kernels, which never form it, and for laying an
+ * 8-bit layer out from it (hxq_quant_fp8_weight), once.
  *   w[n][k] = bf16(C[idx[n][k]] + the sidecar deltas at (n, k)), the deltas
  *   added in fp32 in stored order and the sum rounded once to nearest even
  *   (the value the bf16 matrix-core GEMM uses).
