@@ -488,7 +488,8 @@ int hxq_quant_fp8_weight(const void* w, int w_dtype, uint8_t* q, uint8_t* scales
  * fixed order; bf16 y is rounded once.  A row's result depends on the sizes
  * of the call (they choose the kernel), not on the other rows' values.  A NaN in x makes its
  * whole row of y NaN and no other.  K == 0: y = bias (or 0).
- * Errors: HXQ_ERR_DTYPE; HXQ_ERR_SHAPE (also more than 2^22 tiles of y);
+ * Errors: HXQ_ERR_DTYPE; HXQ_ERR_SHAPE (also more than 2^22 tiles of y, of 256 x
+ * 256 for large products, of 16 x 16 where a gathered x passes 4 GiB);
  * HXQ_ERR_NULL; HXQ_ERR_ALIGN; HXQ_ERR_UNSUPPORTED for a workspace smaller
  * than the query gives. */
 int hxq_linear_fwd_fp8(const void* x, int x_dtype, const uint8_t* x_scales, const uint8_t* wq,

@@ -159,6 +159,19 @@ def test_linear_many_rows(M, N, K, y_dtype):
     check_linear(M, N, K, y_dtype=y_dtype, bias=bool(M % 2), pair=y_dtype == BF16)
 
 
+@pytest.mark.parametrize("pair", [True, False])
+@pytest.mark.parametrize("y_dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", [
+    (2570, 3900, 128), (2700, 3896, 384), (2570, 3900, 1300),  # 256 x 256 tiles, a last one of few rows or a whole one
+    (4200, 3901, 250),  # whole rounds of them, and the rows past those in smaller tiles
+    (2000, 1300, 600),  # 128 x 128 (float32 y), 64 x 128
+    (600, 1100, 3200),  # 64 x 128, the sum split over two workgroups
+    (100, 700, 9000),   # 32 x 64, split
+])
+def test_linear_tiles(M, N, K, y_dtype, pair):
+    check_linear(M, N, K, y_dtype=y_dtype, bias=not pair, pair=pair, seed=9)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 22016, 2048), (8, 2048, 11008), (61, 2048, 11008), (512, 2048, 2048)])
 def test_linear_layer_shapes(M, N, K):
     check_linear(M, N, K, seed=5)
@@ -203,6 +216,40 @@ def test_linear_is_deterministic_and_takes_a_workspace(M, N, K):
         hx.hxq_linear_fwd_fp8(x, None, q, s, b, y2, workspace=w[:0])
 
 
+@pytest.mark.parametrize("M,N,K", [(2, 96, 300), (20, 128, 300), (70, 2048, 256), (2000, 1304, 256), (2570, 3904, 256)])
+@pytest.mark.parametrize("y_dtype", [F32, BF16])
+def test_linear_on_views(M, N, K, y_dtype):
+    """x, y and the bias one element into their storage: results as on their own, nothing beside them written."""
+    x, q, s, b, y = check_linear(M, N, K, x_dtype=F32, y_dtype=y_dtype)
+
+    def shifted(t):
+        store = torch.full((t.numel() + 9,), 7.0, dtype=t.dtype, device="cuda")
+        store[1:1 + t.numel()] = t.flatten()
+        return store, store[1:1 + t.numel()].view(t.shape)
+
+    store, y2 = shifted(torch.zeros_like(y))
+    hx.hxq_linear_fwd_fp8(shifted(x)[1], None, q, s, shifted(b)[1], y2)
+    assert torch.equal(y2, y) and store[0] == 7.0 and (store[-8:] == 7.0).all()
+
+
+def test_norm_on_views():
+    for K in (300, 2048, 2052):
+        x, r, w = make(1, 5, K), make(2, 5, K, dtype=BF16), make(3, K)
+        dy = make(4, 5, K)
+
+        def shifted(t):
+            return torch.cat([t.flatten()[:1], t.flatten()])[1:].view(t.shape)
+
+        got = []
+        for f in (lambda t: t, shifted):
+            out, kept, rstd, dx, dw = torch.empty(5, K, device="cuda"), torch.empty_like(r), torch.empty(5, device="cuda"), torch.empty(5, K, device="cuda"), torch.empty(K, device="cuda")
+            out, kept, rstd, dx, dw = [f(v) for v in (out, kept, rstd, dx, dw)]
+            hx.hxq_rms_norm(f(x), f(w), 1e-6, out, residual=f(r), residual_out=kept, rstd=rstd)
+            hx.hxq_rms_norm_bwd(f(dy), kept, f(w), rstd, dx, dweight=dw)
+            got.append((out, kept, rstd, dx, dw))
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_linear_extreme_scales():
     """Weights and rows whose powers of two are far apart."""
     M, N, K = 20, 140, 384
@@ -240,6 +287,9 @@ CASES = [
     ([2000, 1, 0, 90], 700, 300, 384),
     ([300] * 10, 500, 256, 256),
     ([0, 0, 0], 3, 64, 128),
+    ([5000, 0, 3001, 129, 7000], 4000, 700, 384),  # 256 x 256 tiles, short last ones
+    ([700, 300, 0, 129, 1500], 900, 1400, 640),
+    ([40] * 40, 300, 260, 700),
 ]
 
 
