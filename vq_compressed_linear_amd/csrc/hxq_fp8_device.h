@@ -10,6 +10,15 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kF32 = 0, kBf16 = 1, kE4m3 = 2;  // hxq_dtype
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Two float32 as bf16 bits (nearest, ties to even), a in the low half: one
+// instruction here (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+__device__ __forceinline__ uint16_t to_bf16(float a) { return __builtin_bit_cast(uint16_t, (__bf16)a); }
+
 template <int DT>
 struct Elem;
 template <>
@@ -88,7 +97,7 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&v)[
     };
     P a;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a.u[i] = f32_to_bf16_rne(v[2 * i]) | (f32_to_bf16_rne(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) a.u[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     *reinterpret_cast<P*>(static_cast<uint16_t*>(base) + at) = a;
   }
 }
@@ -104,7 +113,7 @@ __device__ __forceinline__ void store_row8(void* base, int64_t row0, int col, in
         if constexpr (DT == kF32)
           static_cast<float*>(base)[row0 + col + i] = v[i];
         else
-          static_cast<uint16_t*>(base)[row0 + col + i] = (uint16_t)f32_to_bf16_rne(v[i]);
+          static_cast<uint16_t*>(base)[row0 + col + i] = to_bf16(v[i]);
       }
     }
   }
@@ -171,8 +180,6 @@ __device__ __forceinline__ uint2 quant_group(const float (&v)[8], int& byte) {
   byte = e8m0_of(row16_max(m));
   return to_e4m3x8(v, __uint_as_float((uint32_t)(254 - byte) << 23));
 }
-
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // 8 e4m3 bytes times a power of two as bf16 (exact: 4 significant bits).
 __device__ __forceinline__ bf16x8 widen8(int lo, int hi, float p) {

@@ -346,8 +346,8 @@ __device__ __forceinline__ void tile_body(const Fp8Args& a, uint8_t* lds, const 
           if (bias)
 #pragma unroll
             for (int z = 0; z < 4; ++z) v[z] += bias[n + z], u[z] += bias[n + 4 + z];
-          const u32x4 o = {f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16), f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16),
-                           f32_to_bf16_rne(u[0]) | (f32_to_bf16_rne(u[1]) << 16), f32_to_bf16_rne(u[2]) | (f32_to_bf16_rne(u[3]) << 16)};
+          const u32x4 o = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                           pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3])};
           __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.y) + (int64_t)(t.row0 + m0 + r) * a.N + n));
         }
       }

@@ -42,7 +42,7 @@ __device__ __forceinline__ void add_residual(float (&v)[8], const float (&r)[8])
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     v[i] += r[i];
-    if constexpr (RT == kBf16) v[i] = bf16_to_f32(f32_to_bf16_rne(v[i]));
+    if constexpr (RT == kBf16) v[i] = (float)(__bf16)v[i];
   }
 }
 

@@ -85,7 +85,7 @@ __device__ __forceinline__ int64_t fp8_x_row(const Fp8Args& a, int m) {
 
 __device__ __forceinline__ void fp8_store(const Fp8Args& a, int64_t at, float v) {
   if (a.y_bf16)
-    static_cast<uint16_t*>(a.y)[at] = (uint16_t)f32_to_bf16_rne(v);
+    static_cast<uint16_t*>(a.y)[at] = to_bf16(v);
   else
     static_cast<float*>(a.y)[at] = v;
 }
