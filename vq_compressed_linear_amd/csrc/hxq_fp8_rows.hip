@@ -16,7 +16,7 @@
 //
 // Measured: the norm of 25600 rows of 2048 (float32 x, bf16 residual, e4m3 out)
 // 84 us, 5.6 TB/s; one row 2.8 us; the gradient of 2047 rows of 4096 with the
-// weight's 24.8 + 4.2 us (4.7 TB/s in the first launch); conversion of 25600
+// weight's 25 + 3.9 us (4.7 TB/s in the first launch); conversion of 25600
 // rows of 11008 from bf16 156 us, 5.4 TB/s (a large copy: 4.9 TB/s).
 
 #include "hxq_fp8.h"
