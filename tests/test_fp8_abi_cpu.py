@@ -189,6 +189,29 @@ def test_binding_refuses(no_lib, i):
     assert "GPU" not in str(e.value)  # refused for what is wrong with it, not for being on the host
 
 
+def permuted(t):
+    """The same values in other strides, as exchanging two dimensions of another tensor gives them."""
+    u = t.view(torch.uint8).transpose(-1, -2).contiguous().transpose(-1, -2).view(t.dtype)
+    assert not u.is_contiguous() and torch.equal(u.view(torch.uint8), t.view(torch.uint8))
+    return u
+
+
+def test_scales_of_any_strides_are_taken(no_lib):
+    """Refused for being on the host, the last check, and not for their strides; shapes and types still count."""
+    w, s = layer(300, 900)
+    xs = permuted(z(4, 8, dtype=E8))
+    with pytest.raises(ValueError, match="GPU"):
+        F.hxq_linear_fwd_fp8(z(4, 1024, dtype=E4), xs, w, permuted(s), None, z(4, 300))
+    we, se = layer(300, 900, 3)
+    with pytest.raises(ValueError, match="GPU"):
+        F.hxq_linear_fwd_fp8_experts(z(4, 900), None, None, z(4, dtype=torch.int32), we, permuted(se), None, z(4, 300))
+    for bad in (permuted(s)[:2], permuted(s)[:, :4], permuted(s).view(torch.uint8)):
+        with pytest.raises(ValueError, match="w_scales"):
+            F.hxq_linear_fwd_fp8(z(4, 900), None, w, bad, None, z(4, 300))
+    with pytest.raises(ValueError, match="contiguous"):  # the values themselves stay as they are laid out
+        F.hxq_linear_fwd_fp8(z(4, 900), None, permuted(w), s, None, z(4, 300))
+
+
 def test_layer_objects_refuse():
     with pytest.raises(ValueError, match="GPU"):
         hx.Fp8Linear(z(8, 200), device="cpu")

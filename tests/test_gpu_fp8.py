@@ -267,6 +267,37 @@ def test_linear_extreme_scales():
     near(y, Y, 1e-5 * B)
 
 
+@pytest.mark.parametrize("M", [3, 40, 700])
+@pytest.mark.parametrize("E", [None, 3])
+def test_scales_of_any_strides(M, E):
+    """Scales of a transposed weight as exchanging two dimensions leaves them, and of rows likewise: the bytes that
+    contiguous ones give, on the current stream and on another."""
+    N, K = 500, 900  # four blocks of N: nothing is padded, so nothing else would have copied them
+    w = make(1, *(() if E is None else (E,)), N, K, scale=0.02)
+    _, s, wt, st = weight8(w, transposed=True)
+    swapped = s.view(torch.uint8)[..., :8].transpose(-1, -2)  # [blocks of K, blocks of N]
+    assert not swapped.is_contiguous() and torch.equal(swapped, st.view(torch.uint8))
+    dq, ds = rows8(make(2, M, N))
+    loose = ds.view(torch.uint8).t().contiguous().t().view(E8)
+    offsets = None if E is None else torch.tensor([0, M // 3, M // 3, M], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+
+    def product(xs, ws, stream=None):
+        dx = torch.full((M, K), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        if E is None:
+            hx.hxq_linear_fwd_fp8(dq, xs, wt, ws, None, dx, stream=stream)
+        else:
+            hx.hxq_linear_fwd_fp8_experts(dq, xs, None, offsets, wt, ws, None, dx, stream=stream)
+        torch.cuda.synchronize()
+        return dx
+
+    want = product(ds, st)
+    assert not want.isnan().any()
+    for stream in (None, side, side.cuda_stream):
+        assert torch.equal(product(loose, swapped.view(E8), stream), want)
+
+
 # --------------------------------------------------------------------- experts
 
 def routing(seed, counts, Mx, tail=0):

@@ -5,7 +5,10 @@ _binding.
 to a multiple of 128 columns, their scales torch.float8_e8m0fnu tensors whose
 rows are padded with ones to a multiple of 4 (see include/hxq.h).  Every
 function checks shapes, types and devices on the host and raises before the
-library is reached; nothing is computed here.
+library is reached; nothing is computed here.  All tensors are contiguous, but
+for a product's scales: those of a transposed weight, which exchanging two
+dimensions gives with other strides, are copied for the call where they are
+not (one byte for each 16384 of the weight's).
 """
 
 from __future__ import annotations
@@ -48,6 +51,12 @@ def _tensor(t, what: str, dtype, shape) -> None:
             what, dtype, tuple(shape), t.dtype, tuple(t.shape), "" if t.is_contiguous() else ", not contiguous"))
 
 
+def _scales(t, what: str, shape) -> None:
+    """A product's scales: any strides (_laid_out copies)."""
+    if t.dtype is not E8M0 or t.shape != shape:
+        raise ValueError("%s must be a %s %s tensor, got %s %s" % (what, E8M0, tuple(shape), t.dtype, tuple(t.shape)))
+
+
 def _matrix(t, what: str):
     if t.dim() != 2 or not t.is_contiguous():
         raise ValueError("%s must be a contiguous matrix" % what)
@@ -81,6 +90,24 @@ def _stream(stream, dev: int):
     return B._stream(stream, dev)
 
 
+def _queue(stream, dev: int):
+    """Torch's work for a launch goes to the launch's stream, and its allocations belong there: their memory is not
+    handed out again to work that does not wait for the launch."""
+    if stream is None:
+        return _NO_GUARD  # (the device's current one, and _on has made the device current)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(B._stream(stream), dev)
+    return torch.cuda.stream(stream)
+
+
+def _laid_out(t, dev: int, stream):
+    """A product's scales, contiguous; to be kept until the launch is queued."""
+    if t is None or t.is_contiguous():
+        return t
+    with _queue(stream, dev):
+        return t.view(torch.uint8).contiguous()
+
+
 @functools.lru_cache(maxsize=4096)
 def _need(dev: int, query: str, *sizes) -> int:
     """A workspace query's answer for the device (it depends on nothing else)."""
@@ -90,20 +117,14 @@ def _need(dev: int, query: str, *sizes) -> int:
 
 def _workspace(workspace, need: int, what: str, dev: int, stream):
     """(pointer, bytes) of the caller's workspace, or of one from torch's caching allocator; the tensor is the
-    third, to be kept until the launch is queued.  The allocation belongs to the stream of the launch, so its
-    memory is not handed out again to work that does not wait for it."""
+    third, to be kept until the launch is queued."""
     if need < 0:
         raise B.HxqError(need, what)
     if workspace is None:
         if need == 0:
             return None, 0, None
-        if stream is None:
+        with _queue(stream, dev):
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(B._stream(stream), dev)
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
     n = workspace.numel() * workspace.element_size()
@@ -155,7 +176,7 @@ def _activations(x, x_scales, Kp):
             raise ValueError("x has %d columns, the layer's rows %d" % (cols, Kp))
         if x_scales is None:
             raise ValueError("e4m3 x needs its scales")
-        _tensor(x_scales, "x_scales", E8M0, (M, fp8_scale_columns(Kp)))
+        _scales(x_scales, "x_scales", (M, fp8_scale_columns(Kp)))
     else:
         if x_scales is not None:
             raise ValueError("x_scales goes with e4m3 x")
@@ -173,7 +194,7 @@ def hxq_linear_fwd_fp8(x, x_scales, wq, w_scales, bias, y, stream=None, workspac
         raise ValueError("wq must be a contiguous float8_e4m3fn [N, multiple of 128] tensor")
     N, Kp = wq.shape
     M, K, dt = _activations(x, x_scales, Kp)
-    _tensor(w_scales, "w_scales", E8M0, ((N + 127) // 128, fp8_scale_columns(Kp)))
+    _scales(w_scales, "w_scales", ((N + 127) // 128, fp8_scale_columns(Kp)))
     ydt = _dtype(y, "y")
     _tensor(y, "y", y.dtype, (M, N))
     if bias is not None:
@@ -183,6 +204,7 @@ def hxq_linear_fwd_fp8(x, x_scales, wq, w_scales, bias, y, stream=None, workspac
     with _on(dev):
         ptr, size, keep = _workspace(workspace, _need(dev, "hxq_linear_fwd_fp8_workspace", dt, M, N, K),
                                      "hxq_linear_fwd_fp8_workspace", dev, stream)
+        x_scales, w_scales = _laid_out(x_scales, dev, stream), _laid_out(w_scales, dev, stream)
         st = lib.hxq_linear_fwd_fp8(x.data_ptr(), dt, B._ptr(x_scales), wq.data_ptr(), w_scales.data_ptr(),
                                     B._ptr(bias), y.data_ptr(), ydt, M, N, K, ptr, size, _stream(stream, dev))
     if st != B.HXQ_OK:
@@ -199,7 +221,7 @@ def hxq_linear_fwd_fp8_experts(x, x_scales, rows, offsets, wq, w_scales, bias, y
         raise ValueError("wq must be a contiguous float8_e4m3fn [E, N, multiple of 128] tensor")
     E, N, Kp = wq.shape
     Mx, K, dt = _activations(x, x_scales, Kp)
-    _tensor(w_scales, "w_scales", E8M0, (E, (N + 127) // 128, fp8_scale_columns(Kp)))
+    _scales(w_scales, "w_scales", (E, (N + 127) // 128, fp8_scale_columns(Kp)))
     _tensor(offsets, "offsets", torch.int32, (E + 1,))
     M = _matrix(y, "y")[0]
     ydt = _dtype(y, "y")
@@ -215,6 +237,7 @@ def hxq_linear_fwd_fp8_experts(x, x_scales, rows, offsets, wq, w_scales, bias, y
     with _on(dev):
         ptr, size, keep = _workspace(workspace, _need(dev, "hxq_linear_fwd_fp8_experts_workspace", dt, Mx, M, E, N, K),
                                      "hxq_linear_fwd_fp8_experts_workspace", dev, stream)
+        x_scales, w_scales = _laid_out(x_scales, dev, stream), _laid_out(w_scales, dev, stream)
         st = lib.hxq_linear_fwd_fp8_experts(x.data_ptr(), dt, B._ptr(x_scales), B._ptr(rows), offsets.data_ptr(),
                                             wq.data_ptr(), w_scales.data_ptr(), B._ptr(bias), y.data_ptr(), ydt, Mx,
                                             M, E, N, K, ptr, size, _stream(stream, dev))
