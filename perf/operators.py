@@ -113,7 +113,7 @@ def _pad(x, rows, cols):
 def _scales(byte):
     """Exponent bytes as an e8m0 tensor whose rows are padded with ones (byte 127) to a multiple of 4."""
     g = byte.shape[-1]
-    return torch.nn.functional.pad(byte, (0, _up(g, 4) - g), value=127).to(torch.uint8).contiguous().view(E8M0)
+    return torch.nn.functional.pad(byte, (0, _up(g, 4) - g), value=127).to(torch.uint8).view(E8M0)
 
 
 def _weight_8bit(w):
