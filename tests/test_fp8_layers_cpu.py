@@ -1,0 +1,59 @@
+"""The 8-bit layer objects' own work, without a GPU: shapes, and what the backward pass does with the kernels'
+results.  The library's product is replaced by its definition on host tensors, the weight held as it is."""
+
+import pytest
+import torch
+
+import vq_compressed_linear_amd as hx
+from vq_compressed_linear_amd import _binding_fp8 as F
+
+
+def product_of_experts(x, x_scales, rows, offsets, w, w_scales, bias, y, stream=None, workspace=None):
+    """hxq_linear_fwd_fp8_experts by its definition: indices out of range read the nearest row there is."""
+    assert x.dim() == 2 and y.shape[1] == w.shape[1] and (rows is not None or y.shape[0] == x.shape[0])
+    off = offsets.tolist()
+    for e in range(len(off) - 1):
+        for r in range(off[e], off[e + 1]):
+            at = r if rows is None else min(max(int(rows[r]), 0), x.shape[0] - 1)
+            y[r] = w[e] @ x[at] + (0 if bias is None else bias[e])
+
+
+@pytest.fixture
+def experts(monkeypatch):
+    monkeypatch.setattr(F, "hxq_linear_fwd_fp8_experts", product_of_experts)
+    layer = hx.Fp8Experts.__new__(hx.Fp8Experts)
+    g = torch.Generator().manual_seed(1)
+    layer.experts, layer.out_features, layer.in_features = 3, 5, 4
+    layer.wq = torch.randn(3, 5, 4, generator=g)
+    layer.wt = layer.wq.transpose(1, 2).contiguous()
+    layer.w_scales = layer.wt_scales = layer.bias = None
+    return layer
+
+
+def gradient(layer, x, offsets, rows, dy):
+    x = x.clone().requires_grad_()
+    y = layer(x, offsets, rows)
+    y.backward(dy)
+    return y.detach(), x.grad
+
+
+def int32(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("rows", [None, [5, 0, 3], [1, 2, 5, 0], [0, 1, 2, 3, 4, 5], [4, 4, 4, 1, 4, 2, 0]])
+def test_experts_gradient_keeps_the_inputs_shape(experts, rows):
+    """x of more than two dimensions: `rows` index its rows as the forward flattens them."""
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(2, 3, 4, generator=g)
+    n = 6 if rows is None else len(rows)
+    rows = None if rows is None else int32(*rows)
+    offsets = int32(0, n // 2, n // 2, n)
+    dy = torch.randn(n, 5, generator=g)
+    y, dx = gradient(experts, x, offsets, rows, dy)
+    y2, dx2 = gradient(experts, x.reshape(6, 4), offsets, rows, dy)
+    assert torch.equal(y, y2) and dx.shape == x.shape and torch.equal(dx.reshape(6, 4), dx2)
+    want = torch.zeros(6, 4)
+    for r in range(n):
+        want[r if rows is None else int(rows[r])] += dy[r] @ experts.wq[0 if r < n // 2 else 2]
+    assert torch.allclose(dx2, want, rtol=0, atol=1e-5)
