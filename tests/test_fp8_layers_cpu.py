@@ -57,3 +57,28 @@ def test_experts_gradient_keeps_the_inputs_shape(experts, rows):
     for r in range(n):
         want[r if rows is None else int(rows[r])] += dy[r] @ experts.wq[0 if r < n // 2 else 2]
     assert torch.allclose(dx2, want, rtol=0, atol=1e-5)
+
+
+@pytest.mark.parametrize("rows", [[-1, 0, 5, 6], [6, 7, 2**31 - 1, 3], [-(2**31), -7, 1, -6]])
+def test_experts_gradient_of_rows_out_of_range(experts, rows):
+    """An index out of range reads the nearest row there is, and that row receives its gradient."""
+    g = torch.Generator().manual_seed(3)
+    x, dy = torch.randn(6, 4, generator=g), torch.randn(4, 5, generator=g)
+    offsets = int32(0, 1, 1, 4)
+    y, dx = gradient(experts, x, offsets, int32(*rows), dy)
+    y2, dx2 = gradient(experts, x, offsets, int32(*[min(max(r, 0), 5) for r in rows]), dy)
+    assert torch.equal(y, y2) and torch.equal(dx, dx2)
+
+
+def test_experts_gradient_leaves_rows_past_the_last_expert_out(experts):
+    """Their entries in `rows` and in dy may hold anything."""
+    g = torch.Generator().manual_seed(4)
+    x, dy = torch.randn(6, 4, generator=g), torch.randn(5, 5, generator=g)
+    dy[3:] = float("nan")
+    _, dx = gradient(experts, x, int32(0, 1, 1, 3), int32(2, 2, 0, -9, 2**30), dy)
+    want = torch.zeros(6, 4)
+    for r, (e, m) in enumerate([(0, 2), (2, 2), (2, 0)]):
+        want[m] += dy[r] @ experts.wq[e]
+    assert torch.allclose(dx, want, rtol=0, atol=1e-5)
+    _, dx = gradient(experts, x, int32(0, 0, 0, 0), int32(2, 2, 0, -9, 2**30), dy)
+    assert not dx.any()
