@@ -82,3 +82,16 @@ def test_experts_gradient_leaves_rows_past_the_last_expert_out(experts):
     assert torch.allclose(dx, want, rtol=0, atol=1e-5)
     _, dx = gradient(experts, x, int32(0, 0, 0, 0), int32(2, 2, 0, -9, 2**30), dy)
     assert not dx.any()
+
+
+def test_experts_gradient_through_rows_is_not_captured(experts, monkeypatch):
+    """Its sum goes through a sort whose launches are not known to replay: refused inside a graph, before anything
+    of it is queued.  Without `rows` there is no such sum."""
+    x, dy = torch.ones(6, 4), torch.ones(6, 5)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="captured"):
+        gradient(experts, x, int32(0, 2, 4, 6), int32(0, 1, 2, 3, 4, 5), dy)
+    gradient(experts, x, int32(0, 2, 4, 6), None, dy)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    gradient(experts, x, int32(0, 2, 4, 6), int32(0, 1, 2, 3, 4, 5), dy)

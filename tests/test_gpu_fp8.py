@@ -639,6 +639,49 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
 
 
+def test_gradients_captured_and_replayed():
+    """Forward and backward of the layers in one graph, inputs changed between replays, the same work eagerly (on
+    leaves of its own) in between."""
+    T, K, N, E = 9, 512, 640, 3
+    layer = hx.Fp8Linear(make(4, N, K, scale=0.05), train=True)
+    experts = hx.Fp8Experts(make(5, E, K, N, scale=0.05), train=True)
+    offsets = torch.tensor([0, 4, 4, 7], dtype=torch.int32, device="cuda")
+    dy = make(6, T, K)
+
+    def leaves():
+        return (make(1, T, K).requires_grad_(), make(2, T, K, dtype=BF16).requires_grad_(),
+                hx.RmsNorm((1 + 0.1 * make(3, K)).requires_grad_()))
+
+    def step(x, res, norm):
+        y, h = norm(x, res)
+        z = experts(layer(y), offsets)
+        return (z.detach(), *torch.autograd.grad((z, h), (x, res, norm.weight), (dy, dy.bfloat16())))
+
+    mine, eager = leaves(), leaves()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*mine)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*mine)
+    for i in range(4):
+        new = make(10 + i, T, K)
+        with torch.no_grad():
+            mine[0].copy_(new)
+            eager[0].copy_(new)
+        dy.copy_(make(20 + i, T, K))
+        offsets.copy_(torch.tensor([0, i, 5, 5 + i], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        have = [t.clone() for t in got]
+        for a, b in zip(have, step(*eager)):
+            assert torch.equal(a, b) and not a.isnan().any()
+        torch.cuda.synchronize()
+
+
 def test_on_another_stream():
     """Calls given a stream run there; two streams at once, each with a workspace of its own."""
     N, K = 2048, 2048
