@@ -95,3 +95,34 @@ def test_experts_gradient_through_rows_is_not_captured(experts, monkeypatch):
     gradient(experts, x, int32(0, 2, 4, 6), None, dy)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     gradient(experts, x, int32(0, 2, 4, 6), int32(0, 1, 2, 3, 4, 5), dy)
+
+
+def product(x, x_scales, w, w_scales, bias, y, stream=None, workspace=None):
+    y.copy_(x @ w.t() + (0 if bias is None else bias))
+
+
+@pytest.mark.parametrize("N,K", [(5, 0), (0, 4), (0, 0), (5, 4)])
+@pytest.mark.parametrize("lead", [(3,), (2, 3), (0,), (2, 0)])
+def test_linear_of_no_features(monkeypatch, lead, N, K):
+    """Without a sum y is the bias, without outputs it is empty; the gradients likewise."""
+    monkeypatch.setattr(F, "hxq_linear_fwd_fp8", product)
+    layer = hx.Fp8Linear.__new__(hx.Fp8Linear)
+    layer.out_features, layer.in_features, layer.bias = N, K, torch.arange(N).float()
+    layer.wq = torch.ones(N, K)
+    layer.wt, layer.w_scales, layer.wt_scales = layer.wq.t().contiguous(), None, None
+    x = torch.ones(*lead, K, requires_grad=True)
+    y = layer(x)
+    assert torch.equal(y, (layer.bias + K).expand(*lead, N))
+    y.backward(torch.ones_like(y))
+    assert torch.equal(x.grad, torch.full((*lead, K), float(N)))
+
+
+@pytest.mark.parametrize("lead", [(3,), (2, 3), (0,)])
+def test_norm_of_no_columns(monkeypatch, lead):
+    monkeypatch.setattr(F, "hxq_rms_norm", lambda *a, **k: None)
+    monkeypatch.setattr(F, "hxq_rms_norm_bwd", lambda *a, **k: None)
+    x, r = torch.ones(*lead, 0, requires_grad=True), torch.ones(*lead, 0, requires_grad=True)
+    out, h = hx.RmsNorm(torch.ones(0), device="cpu")(x, r)
+    assert out.shape == h.shape == x.shape
+    torch.autograd.backward((out, h), (torch.ones_like(out), torch.ones_like(h)))
+    assert x.grad.shape == r.grad.shape == x.shape

@@ -187,6 +187,28 @@ def test_linear_without_a_sum():
     hx.hxq_linear_fwd_fp8(torch.zeros((0, 0), device="cuda"), None, w, s, None, y[:0])
 
 
+def test_layers_of_no_features():
+    """A sum over nothing is the bias, its gradient has no columns; no outputs: a gradient of zeros."""
+    b = make(1, 5)
+    layer = hx.Fp8Linear(torch.zeros((5, 0), device="cuda"), b, train=True)
+    x = torch.zeros((2, 3, 0), device="cuda", requires_grad=True)
+    y = layer(x)
+    assert torch.equal(y, b.expand(2, 3, 5))
+    y.backward(torch.ones_like(y))
+    assert x.grad.shape == x.shape
+    none = hx.Fp8Linear(torch.zeros((0, 5), device="cuda"), train=True)
+    x = make(2, 3, 5).requires_grad_()
+    y = none(x)
+    assert y.shape == (3, 0)
+    y.backward(torch.ones_like(y))
+    assert not x.grad.any()
+    z = torch.zeros((2, 3, 0), device="cuda", requires_grad=True)
+    out, h = hx.RmsNorm(torch.zeros(0, device="cuda"))(z, z)
+    assert out.shape == h.shape == z.shape
+    h.sum().backward()
+    assert z.grad.shape == z.shape
+
+
 @pytest.mark.parametrize("M", [1, 20, 60, 300])
 def test_linear_with_nan_rows_keeps_them_apart(M):
     """A NaN (or infinity) in x makes its own row of y NaN and no other."""
