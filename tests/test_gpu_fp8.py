@@ -272,6 +272,119 @@ def test_norm_on_views():
         assert all(torch.equal(a, b) for a, b in zip(*got))
 
 
+# Shapes that reach every kernel, with more than four 128-blocks of k (so that a word of scales is left behind): few
+# rows, 32 x 64 tiles without and with a split sum, 64 x 128 without and with one, 128 x 128 (float32 y), 256 x 256
+# with a last one of few rows, and whole rounds of those with the rest in smaller tiles.
+EVERY_KERNEL = [(3, 200, 700), (300, 260, 640), (100, 700, 9000), (600, 1100, 3200), (2000, 1300, 600),
+                (2570, 3900, 1300), (4200, 3901, 700)]
+
+
+def whole(seed, K, *rows):
+    """e4m3 values that are eighths of whole numbers, 8 to 15 of either sign or zero: (bytes, the whole numbers)."""
+    g = torch.Generator().manual_seed(seed)
+    v = torch.randint(8, 16, (*rows, K), generator=g) * (torch.randint(0, 2, (*rows, K), generator=g) * 2 - 1)
+    v[torch.rand(*rows, K, generator=g) < 0.1] = 0
+    v = torch.nn.functional.pad(v, (0, up(K, 128) - K))
+    return (v / 8).to(E4).cuda(), v.double().cuda()
+
+
+def powers(seed, far, sign, *shape):
+    """Exponents [..., blocks of k]: 0 or 1, plus `sign` times a block's own, up to `far` either way."""
+    own = torch.randint(-far, far + 1, shape[-1:], generator=torch.Generator().manual_seed(7)) if far else 0
+    e = torch.randint(0, 2, shape, generator=torch.Generator().manual_seed(seed)) + sign * own
+    pad = torch.nn.functional.pad(e + 127, (0, up(shape[-1], 4) - shape[-1]), value=127)
+    return pad.to(torch.uint8).view(E8).cuda(), torch.exp2(e.double()).cuda()
+
+
+def spread(p, rows):
+    """A power for every element, from one for each 128 columns (and, with `rows`, each 128 rows)."""
+    p = p.repeat_interleave(128, -1)
+    return p if rows is None else p.repeat_interleave(128, -2)[..., :rows, :]
+
+
+@pytest.mark.parametrize("far", [0, 100])
+@pytest.mark.parametrize("y_dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", EVERY_KERNEL)
+def test_linear_of_whole_numbers_is_exact(M, N, K, y_dtype, far):
+    """Products of the values are whole multiples of 2^-6 from 64 to 225 or zero, so no group of 8 holds one below
+    2^-8 of its largest, and the 8-bit matrix cores keep them whole; powers of two make them 1 to 4 times that,
+    their own (2^a for x, 2^-a for w, |a| <= far) cancel, and B, the sum of the magnitudes, stays below 2^24
+    of the smallest step: every partial sum is exact in float32, and y is the exact sum, rounded once."""
+    say("exact", M, N, K, y_dtype, far)
+    G = -(-K // 128)
+    (xq, X), (wq, W) = whole(M, K, M), whole(N, K, N)
+    (xs, xp), (ws, wp) = powers(1, far, 1, M, G), powers(2, far, -1, -(-N // 128), G)
+    b = torch.randint(-999, 999, (N,), generator=torch.Generator().manual_seed(3)).float().cuda() / 64
+    X, W = X * spread(xp, None), W * spread(wp, N)
+    assert (X.abs() @ W.abs().t()).max() + 999 < 2**24
+    want = ((X @ W.t()) / 64 + b).float()
+    y = torch.full((M, N), float("nan"), dtype=y_dtype, device="cuda")
+    hx.hxq_linear_fwd_fp8(xq, xs, wq, ws, b, y)
+    assert torch.equal(y, want.to(y_dtype))
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("y_dtype", [F32, BF16])
+@pytest.mark.parametrize("counts,Mx,N,K", [([1, 0, 1, 1, 2], 4, 300, 700), ([40] * 20 + [0, 3], 300, 260, 700),
+                                           ([300] * 10, 500, 256, 1300), ([5000, 0, 3001, 129, 7000], 4000, 700, 640),
+                                           ([5000, 0, 3001, 129, 7000], 4000, 300, 700),
+                                           ([3, 0, 2], 4, 48, 9000)])
+def test_experts_of_whole_numbers_are_exact(counts, Mx, N, K, y_dtype, gather):
+    """The same for rows grouped by expert."""
+    say("exact experts", counts[:5], Mx, N, K, y_dtype, gather)
+    M, E, G = sum(counts), len(counts), -(-K // 128)
+    rows, offsets = routing(M, counts, Mx)
+    if not gather:
+        rows, Mx = None, M
+    (xq, X), (wq, W) = whole(M, K, Mx), whole(N, K, E, N)
+    (xs, xp), (ws, wp) = powers(1, 100, 1, Mx, G), powers(2, 100, -1, E, -(-N // 128), G)
+    X, W = X * spread(xp, None), W * spread(wp, N)
+    want, off = torch.empty((M, N), device="cuda"), offsets.tolist()
+    for e in range(E):
+        at = slice(off[e], off[e + 1])
+        x = X[at] if rows is None else X[rows[at].long()]
+        assert not len(x) or (x.abs() @ W[e].abs().t()).max() < 2**24
+        want[at] = ((x @ W[e].t()) / 64).float()
+    y = torch.full((M, N), float("nan"), dtype=y_dtype, device="cuda")
+    hx.hxq_linear_fwd_fp8_experts(xq, xs, rows, offsets, wq, ws, None, y)
+    assert torch.equal(y, want.to(y_dtype))
+
+
+@pytest.mark.parametrize("y_dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", EVERY_KERNEL)
+def test_every_kernel_keeps_nan_rows_apart(M, N, K, y_dtype):
+    """test_linear_with_nan_rows_keeps_them_apart in every kernel, as an infinity, a NaN and both, in the first, an
+    inner and the last row."""
+    say("nan", M, N, K, y_dtype)
+    x, (q, s) = make(1, M, K, dtype=BF16), weight8(make(2, N, K, scale=0.02))
+    y, y2 = [torch.full((M, N), 7.0, dtype=y_dtype, device="cuda") for _ in range(2)]
+    hx.hxq_linear_fwd_fp8(x, None, q, s, None, y)
+    assert y.isfinite().all()
+    bad = torch.zeros(M, dtype=torch.bool, device="cuda")
+    x[0, K - 1], x[M // 2, K // 2], x[M - 1, 0], x[M - 1, 1] = float("inf"), float("nan"), -float("inf"), float("nan")
+    bad[[0, M // 2, M - 1]] = True
+    hx.hxq_linear_fwd_fp8(x, None, q, s, None, y2)
+    assert torch.equal(y2[~bad], y[~bad]) and y2[bad].isnan().all()
+
+
+@pytest.mark.parametrize("y_dtype", [F32, BF16])
+@pytest.mark.parametrize("counts", [[1, 0, 1, 1], [40] * 20, [300, 0, 290, 310], [5000, 0, 3001, 129, 7000]])
+def test_experts_keep_nan_rows_apart(counts, y_dtype):
+    """A NaN in a row of x reaches the rows of y that read it and no other; rows past the last expert's stay."""
+    Mx, N, K, M = 50, 300, 700, sum(counts)
+    say("nan experts", counts[:5], y_dtype)
+    rows, offsets = routing(5, counts, Mx, 3)
+    rows[0] = 17
+    x, (q, s) = make(1, Mx, K), weight8(make(2, len(counts), N, K, scale=0.02))
+    y, y2 = [torch.full((M + 3, N), 7.0, dtype=y_dtype, device="cuda") for _ in range(2)]
+    hx.hxq_linear_fwd_fp8_experts(x, None, rows, offsets, q, s, None, y)
+    x[17, K - 1] = float("nan")
+    hx.hxq_linear_fwd_fp8_experts(x, None, rows, offsets, q, s, None, y2)
+    bad = rows == 17
+    bad[M:] = False
+    assert torch.equal(y2[~bad], y[~bad]) and y2[bad].isnan().all() and (y2[M:] == 7.0).all()
+
+
 def test_linear_extreme_scales():
     """Weights and rows whose powers of two are far apart."""
     M, N, K = 20, 140, 384
@@ -722,6 +835,40 @@ def test_on_another_stream():
         hx.hxq_linear_fwd_fp8(x, None, q, s, None, y, stream=st.cuda_stream)
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("out_dtype,res", [(F32, BF16), (BF16, F32), (E4, BF16), (E4, None)])
+def test_norm_of_more_rows_than_a_launch(out_dtype, res):
+    """2^22 rows to a launch: the second one's rows are those that a call of their own gives."""
+    M, K, cut = 2**22 + 3, 5, 2**22
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(M, K, generator=g, device="cuda")
+    r = None if res is None else torch.randn(M, K, generator=g, device="cuda").to(res)
+    w = make(2, K)
+
+    def norm(*at):
+        n = len(range(M)[slice(*at)])
+        out = torch.full((n, 128 if out_dtype == E4 else K), 3.0, device="cuda").to(out_dtype)
+        scales = torch.full((n, 4), 9, dtype=torch.uint8, device="cuda").view(E8) if out_dtype == E4 else None
+        kept = None if res is None else torch.full((n, K), 3.0, dtype=res, device="cuda")
+        rstd = torch.full((n,), 3.0, device="cuda")
+        hx.hxq_rms_norm(x[slice(*at)], w, 1e-6, out, scales=scales, residual=None if r is None else r[slice(*at)],
+                        residual_out=kept, rstd=rstd)
+        return [t if t.dtype not in (E4, E8) else t.view(torch.uint8) for t in (out, scales, kept, rstd) if t is not None]
+
+    for whole_, first, last in zip(norm(0, M), norm(0, cut), norm(cut, M)):
+        assert torch.equal(whole_[:cut], first) and torch.equal(whole_[cut:], last)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_of_more_groups_than_a_launch(dtype):
+    """2^26 groups of a row of scales to a launch, four to a row here."""
+    cut = 2**24
+    x = torch.randn(cut + 5, 1, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(dtype)
+    (q, s), (q1, s1), (q2, s2) = [[t.view(torch.uint8) for t in rows8(v)] for v in (x, x[:cut], x[cut:])]
+    assert torch.equal(q[:cut], q1) and torch.equal(s[:cut], s1) and torch.equal(q[cut:], q2) and torch.equal(s[cut:], s2)
+    Q, S = O.quant_rows(host(x[cut:]))
+    assert np.array_equal(q2.cpu().numpy(), Q) and np.array_equal(s2.cpu().numpy(), S)
 
 
 def test_rows_past_32_bits():
