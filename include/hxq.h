@@ -481,13 +481,19 @@ int hxq_quant_fp8_weight(const void* w, int w_dtype, uint8_t* q, uint8_t* scales
  *             entry ignored and on return unspecified.  Two calls that may run
  *             at once need one each, captured graphs among them.
  * Arithmetic: with float32 y the 8-bit values are multiplied exactly and
- * summed in fp32 (widened to bf16, on the bf16 matrix cores).  With bf16 y
+ * summed in fp32 (widened to bf16, on the bf16 matrix cores).  Widened, a
+ * value with its power of two below 2^-130 in magnitude is rounded to a
+ * multiple of 2^-133, and one past float32's largest is an infinity (e4m3
+ * rounds 248 * 2^120 = 3.297e38 and more up to 2^128).  With bf16 y
  * the 8-bit matrix cores may multiply, at twice the rate: they keep a product
  * only down to 2^-13 of the largest of its group of 8 (1.5e-5 of the result,
- * measured; bf16's own rounding is 2^-9 of it).  Partial sums are added in a
+ * measured; at most 2^-10 of |x| |w|^T.  bf16's own rounding is up to 2^-8 of
+ * it).  A caller who wants bf16 of the exact products' sum takes float32 y and
+ * rounds that.  Partial sums are added in a
  * fixed order; bf16 y is rounded once.  A row's result depends on the sizes
- * of the call (they choose the kernel), not on the other rows' values.  A NaN in x makes its
- * whole row of y NaN and no other.  K == 0: y = bias (or 0).
+ * of the call (they choose the kernel: a row in a batch of 8 and the same row
+ * in one of 80 may differ in the last bits), not on the other rows' values.
+ * A NaN in x makes its whole row of y NaN and no other.  K == 0: y = bias (or 0).
  * Errors: HXQ_ERR_DTYPE; HXQ_ERR_SHAPE (also more than 2^22 tiles of y, of 256 x
  * 256 for large products, of 16 x 16 where a gathered x passes 4 GiB);
  * HXQ_ERR_NULL; HXQ_ERR_ALIGN; HXQ_ERR_UNSUPPORTED for a workspace smaller
@@ -518,8 +524,9 @@ int64_t hxq_linear_fwd_fp8_workspace(int x_dtype, int64_t M, int64_t N, int64_t 
  *   bias      [E][N] or NULL; the rest as for hxq_linear_fwd_fp8.
  * The input gradient is the same call with dy as x, rows NULL and the
  * transposed copies.
- * Errors: those of hxq_linear_fwd_fp8; HXQ_ERR_SHAPE for E outside 1 .. 65535
- * or M_x != M without rows. */
+ * Errors: those of hxq_linear_fwd_fp8; HXQ_ERR_SHAPE for E outside 1 .. 65535,
+ * for M_x != M without rows, or for rows of y that no x is given for (M_x == 0,
+ * M > 0). */
 int hxq_linear_fwd_fp8_experts(const void* x, int x_dtype, const uint8_t* x_scales, const int32_t* rows,
                                const int32_t* offsets, const uint8_t* wq, const uint8_t* w_scales, const float* bias,
                                void* y, int y_dtype, int64_t M_x, int64_t M, int64_t E, int64_t N, int64_t K,

@@ -385,6 +385,23 @@ def test_experts_keep_nan_rows_apart(counts, y_dtype):
     assert torch.equal(y2[~bad], y[~bad]) and y2[bad].isnan().all() and (y2[M:] == 7.0).all()
 
 
+@pytest.mark.parametrize("y_dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N", [(2, 40), (40, 200), (300, 260), (2000, 1300), (2570, 3900)])
+def test_linear_at_the_ends_of_the_range(M, N, y_dtype):
+    """The largest values that e4m3 holds below 2^128 and the smallest that bf16 holds whole, beside weights of
+    zero: one product to a sum, so y is that product."""
+    K = 300
+    x, w = torch.zeros((M, K), device="cuda"), torch.zeros((N, K), device="cuda")
+    x[:, 0], w[::2, 0] = 240 * 2.0**120, 1.75 * 2.0**-5
+    x[::2, 140], w[1::2, 140] = 1.875 * 2.0**-130, -1.25 * 2.0**120
+    y = torch.full((M, N), float("nan"), dtype=y_dtype, device="cuda")
+    hx.hxq_linear_fwd_fp8(x, None, *weight8(w), None, y)
+    want = torch.zeros((M, N), dtype=torch.float64)
+    want[:, ::2] = 240 * 1.75 * 2.0**115
+    want[::2, 1::2] = -1.875 * 1.25 * 2.0**-10
+    assert torch.equal(y, want.float().to(y_dtype).cuda())
+
+
 def test_linear_extreme_scales():
     """Weights and rows whose powers of two are far apart."""
     M, N, K = 20, 140, 384
