@@ -79,7 +79,7 @@ hxq::Fp8Plan plan(bool y_bf16, int64_t Mx, int64_t M, int64_t N, int64_t K, int6
     p.S = wgs < cus && blocks >= 48 ? (int)std::min<int64_t>((2 * cus + wgs - 1) / wgs, blocks / 16) : 1;
     p.waves = wgs >= 2 * cus || blocks < 16 ? 4 : p.S > 1 || wgs >= cus || blocks < 32 ? 8 : 16;
     // many workgroups: two blocks of each wave in flight (22016 x 2048: 10.8 against 11.5 us), else one, which
-    // leaves room for more waves (8512 x 2048: 6.4 against 7.0)
+    // leaves room for more waves (8512 x 2048: 6.4 against 7.0); at four to a CU (16384 x 2048) 10.7 us either way
     p.depth = wgs > 4 * cus ? 2 : 1;
   }
   p.kbs = (int)((blocks + p.S - 1) / p.S);

@@ -15,13 +15,14 @@
 //     matrix rate.
 //
 // Bound: the matrix cores for the large tiles, the weight's bytes for the small
-// ones.  Measured: 8192^3 in 403-417 us with bf16 y (2.6-2.7 PFLOP/s), 743-757
-// us with float32 y (1.45-1.48); gate|up (22016 x 2048) at 2048 rows 88 us with
-// bf16 y; 64 experts of 2048 x 2048 with 8 rows each 52 us from memory (5.1
-// TB/s).  In the large tile the matrix cores are busy for 78% of the CUs' time
-// at 8192^3 (64 stages) and 46% at 16 stages: a stage takes 1.4 us, a tile's
-// start and its output (every CU stores 128 KB at once) some 10 us.  No LDS bank
-// conflicts in the loop.  Four waves of 128 x 128 instead of eight of 128 x 64
+// ones.  Measured: 8192^3 in 411-414 us with bf16 y (2.7 PFLOP/s), 745-761 us
+// with float32 y (1.45-1.48); gate|up (22016 x 2048) at 2048 rows 88-90 us with
+// bf16 y; 64 experts of 2048 x 2048 with 8 rows each 54 us from memory (5.0
+// TB/s).  In the large tile the matrix cores are busy for 74% of the CUs' time
+// at 8192^3 (64 stages; 82% with float32 y), 57% at gate|up's 16 stages and 45%
+// with experts' ragged rows there: a stage takes 1.4 us, a tile's start and its
+// output (every CU stores 128 KB at once) some 8 to 10 us.  No LDS bank conflicts
+// in the loop.  Four waves of 128 x 128 instead of eight of 128 x 64
 // read a third less LDS but leave nothing to run behind a wait (8192^3 485
 // against 428 us); rings of four to seven stages gained nothing for the small
 // tiles; s_setprio around the matrix ops cost 1-2%.

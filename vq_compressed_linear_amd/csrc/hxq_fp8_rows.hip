@@ -14,10 +14,13 @@
 // held by 16 lanes of one DPP row, whose largest magnitude needs no LDS.
 // Rows wider than 12288 columns are read a second time (from the caches).
 //
-// Measured: the norm of 25600 rows of 2048 (float32 x, bf16 residual, e4m3 out)
-// 84 us, 5.6 TB/s; one row 2.8 us; the gradient of 2047 rows of 4096 with the
-// weight's 25 + 3.9 us (4.7 TB/s in the first launch); conversion of 25600
-// rows of 11008 from bf16 156 us, 5.4 TB/s (a large copy: 4.9 TB/s).
+// Measured, inputs from memory: the norm of 25600 rows of 2048 (float32 x, bf16
+// residual, e4m3 out) 84 us, 5.6 TB/s; one row 2.3 us; the gradient of 2047
+// rows of 4096 with the weight's 28 + 4.0 us (4.2 TB/s in the first launch);
+// conversion of 25600 rows of 11008 from bf16 157 us, 5.4 TB/s (a large copy:
+// 4.9 TB/s).  A weight of 22016 x 2048 from bf16 in 107 us (1.3 TB/s), with its
+// transposed copy 114: a layer is laid out once, so its bytes leave LDS one at
+// a time and nothing was made faster.
 
 #include "hxq_fp8.h"
 #include "hxq_fp8_device.h"
@@ -144,7 +147,10 @@ template <int XT, int RT, int OT>
 void norm_launch(const NormArgs& a, hipStream_t s) {
   const int K = a.K;
   // A wave to a short row (25600 x 512: 21 us, 32 with a workgroup), else a workgroup: a wave with four chunks of
-  // a row of 2048 took 92 us against 84 at 25600 rows, 8.3 against 3.8 at 256.
+  // a row of 2048 took 92 us against 84 at 25600 rows, 8.3 against 3.8 at 256.  As many chunks as the row has up to
+  // two (20480 x 2560: 101 us, 125 with room for six; 12800 x 4096: 102, 104), then six (with fewer no faster:
+  // 10240 x 5120 102 us, 104 with three; 6400 x 8192 99, 102 with four) rather than a second reading (105, 107;
+  // 4266 x 12288: 103, 117).
   const unsigned rows = (unsigned)a.M, rows4 = (unsigned)((a.M + 3) / 4);
   if (K <= 512)
     hipLaunchKernelGGL((rms_norm_rows<64, 1, XT, RT, OT>), dim3(rows4), dim3(256), 0, s, a);
@@ -335,7 +341,10 @@ __global__ __launch_bounds__(1024) void norm_dw_sum(const float* part, float* dw
   dw[o] = sum;
 }
 
-// A wave to a short row, else a workgroup (20000 x 2048: 83 us, 96 with a wave to a row).
+// A wave to a short row, else a workgroup (20000 x 2048: 83 us, 96 with a wave to a row).  Two chunks up to 4096
+// columns (20480 x 2560: 121 us, 229 with room for six; 12800 x 4096: 104, 168), then six rather than a second reading
+// (10240 x 5120: 169 us, 279; 6400 x 8192: 146, 244; 4266 x 12288: 141, 251).  Six cost widths well below 12288 more
+// than they need: with three chunks 10240 x 5120 took 112 us, with four 6400 x 8192 112.
 bool bwd_waves(int64_t K) { return K <= 512; }
 
 template <int DT, int HT>

@@ -22,10 +22,12 @@
 // is split over workgroups as well leaves its parts in the workspace for
 // fp8_sum.
 //
-// Measured, one row of x (bf16, converted in the kernel), weights rotating
-// through memory: 22016 x 2048 in 10.5 us (4.3 TB/s; a plain read of those
-// bytes takes 8.8), 8512 x 2048 6.4, 2048 x 2048 4.4, 2048 x 11008 10.2 (two
-// launches); 8 experts of 64, 2048 x 2048 each, 9.6 us.
+// Measured, one row of x (bf16, converted in the kernel), the weights of enough
+// layers in turn that they come from memory: 22016 x 2048 in 10.2 us (4.4 TB/s;
+// a plain read of those bytes takes 8.8), 8512 x 2048 7.5, 2048 x 2048 5.2,
+// 2048 x 11008 8.7 + 1.8 (two launches); 8 experts of 64, 2048 x 2048 each,
+// 10.3 us.  (The figures that the plan's rules give are of weights that the
+// last-level cache holds in part, the same for both sides of each.)
 
 #include "hxq_fp8.h"
 #include "hxq_fp8_device.h"
