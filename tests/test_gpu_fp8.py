@@ -791,6 +791,34 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
 
 
+def test_scales_of_any_strides_captured():
+    """The copy of permuted scales is part of a graph: replays see the scales as they are then."""
+    N, K, M = 300, 512, 40  # one row of scales for each 128 of N, four blocks of K: no padding either way
+    w, s = weight8(make(1, N, K, scale=0.02))
+    loose = s.view(torch.uint8).t().contiguous().t()
+    x, y = make(2, M, K), torch.empty((M, N), device="cuda")
+
+    def step(scales, out):
+        hx.hxq_linear_fwd_fp8(x, None, w, scales.view(E8), None, out)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(loose, y)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(loose, y)
+    for i in range(4):
+        loose += i
+        graph.replay()
+        torch.cuda.synchronize()
+        have, want = y.clone(), torch.empty_like(y)
+        step(loose.contiguous(), want)
+        assert torch.equal(have, want) and not have.isnan().any()
+        torch.cuda.synchronize()
+
+
 def test_gradients_captured_and_replayed():
     """Forward and backward of the layers in one graph, inputs changed between replays, the same work eagerly (on
     leaves of its own) in between."""
